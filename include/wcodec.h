@@ -458,11 +458,143 @@ int wc_decompress_tans_batch(const wc_batch_item *h_items, uint32_t count, int32
                              void *stream);
 
 /*
+ * 4-bit streams with group scales (header flags 8). The lossy sibling of the
+ * streams above, for weights that sit on a 4-bit grid:
+ *   W[r][c] = s[r][g] * (q[r][c] - z[r][g]),   g = c / group
+ * with codes q and zero points z in 0..15 (z = 8 without WC_Q4_ZEROS) and
+ * 16-bit scales s. group is 32, 64 or 128 columns (the last group of a row may
+ * be shorter); any number of rows and columns up to the limits below. The
+ * pages have no counterpart but name the setting ("MINE: Entropy-coded
+ * Memory-efficient Inference for Large Language Models", Abstract: quantized
+ * weights, where fewer bytes per weight are the speed of single-stream
+ * decoding); the layout is this library's.
+ * Layout: the 128-byte container header (group in the block field, flags 8,
+ * + 16 with zero points, + 32 with FP16 scales, rows and cols at bytes 88 and
+ * 92), then records of 16 rows x 128 columns: 1024 bytes of codes (32-bit
+ * words [t 0..3][row][i 0..3], word (t, i) holding columns 32 i + 8 t + (0..7),
+ * element e in nibble (e >> 1) + 4 (e & 1)), the scales u16 [128 / group][16],
+ * and with zero points u8 [128 / group][16], padded to 32 bytes; ordered
+ * [128-row block][128-column slice][16-row block].
+ *
+ *  wc_q4_bytes       the stream's exact size; 0 if an argument is invalid
+ *  wc_q4_quantize    rounds rows x cols 16-bit weights (rows ld elements apart,
+ *                    2-byte aligned; BF16, or FP16 with WC_Q4_SCALES_FP16: the
+ *                    scales have the weights' type) to a stream at d_out. Per
+ *                    row and group, to nearest even:
+ *                      s = round16(max|w| / 7), q = clamp(rint(w/s), -8, 7) + 8
+ *                    or, with WC_Q4_ZEROS, lo = min(w, 0), hi = max(w, 0),
+ *                      s = round16((hi - lo) / 15), z = clamp(rint(-lo/s), 0, 15),
+ *                      q = clamp(rint(w/s) + z, 0, 15)
+ *                    s = 0: every code stands for zero. A NaN in a group makes
+ *                    its scale NaN; an infinity makes it infinite.
+ *  wc_q4_pack        the stream of given codes (u8, rows x cols, low 4 bits
+ *                    used), scales (u16, rows x groups) and zero points (u8,
+ *                    rows x groups; with WC_Q4_ZEROS, else NULL), all dense:
+ *                    nothing is rounded
+ *  wc_q4_dequantize  s * (q - z) rounded once to dtype (exact in FP32), rows ld
+ *                    elements apart
+ *  wc_q4_gemm        y[p][r] = sum_g s[r][g] * sum_{c in g} (q - z) * x[p][c]
+ *                    for p < tokens. x: BF16, or FP16 with WC_Q4_X_FP16; rows
+ *                    ldx elements apart. y: FP32, or x's type with
+ *                    WC_Q4_Y_16BIT (one rounding); rows ldy elements apart.
+ *                    Both aligned to their elements; 16-byte aligned rows of x
+ *                    are faster. The codes enter the matrix instructions as
+ *                    exact integers and each group's FP32 sum is scaled in
+ *                    FP32, so no scaled weight is rounded. Sums are taken in a
+ *                    fixed order: the same bits on every run. A product with a
+ *                    0 code follows the formula: 0 * Inf is NaN.
+ *  wc_q4_gemm_experts  the same for `experts` matrices of one shape, their
+ *                    streams stream_stride bytes apart (a multiple of 16, at
+ *                    least wc_q4_bytes): rows d_offsets[e] .. d_offsets[e+1]-1
+ *                    of x (as wc_moe_sort leaves them) take matrix e. `tokens`
+ *                    bounds the rows of x and y; offsets are clamped to it, and
+ *                    rows outside every range are neither read nor written.
+ * The expanding calls check the header on the device (WC_ERR_CORRUPT_STREAM in
+ * *d_status; the output is then unspecified); a stream shorter than its size
+ * returns WC_ERR_CORRUPT_STREAM without launching. Nothing is read outside the
+ * stated buffers whatever they hold.
+ */
+#define WC_Q4_ZEROS 1u
+#define WC_Q4_SCALES_FP16 2u
+#define WC_Q4_X_FP16 4u
+#define WC_Q4_Y_16BIT 8u
+#define WC_Q4_MAX_ROWS (1u << 22)
+#define WC_Q4_MAX_COLS (1u << 20)
+#define WC_Q4_MAX_TOKENS (1u << 24)
+#define WC_MOE_MAX_EXPERTS 1024u
+#define WC_MOE_MAX_SLOTS 0x7FFFFFE0u
+#define WC_MOE_MAX_COLS (1u << 24)
+#define WC_DTYPE_BF16 0u
+#define WC_DTYPE_FP16 1u
+#define WC_DTYPE_FP32 2u
+uint64_t wc_q4_bytes(uint64_t rows, uint64_t cols, uint32_t group, uint32_t flags);
+int wc_q4_quantize(const void *d_w, uint64_t ld, uint64_t rows, uint64_t cols, uint32_t group,
+                   uint32_t flags, void *d_out, uint64_t out_capacity, void *stream);
+int wc_q4_pack(const uint8_t *d_codes, const void *d_scales, const uint8_t *d_zeros,
+               uint64_t rows, uint64_t cols, uint32_t group, uint32_t flags, void *d_out,
+               uint64_t out_capacity, void *stream);
+int wc_q4_dequantize(const void *d_stream, uint64_t stream_bytes, uint64_t rows, uint64_t cols,
+                     uint32_t group, uint32_t flags, void *d_out, uint64_t ld, uint32_t dtype,
+                     int32_t *d_status, void *stream);
+int wc_q4_gemm(const void *d_stream, uint64_t stream_bytes, uint64_t rows, uint64_t cols,
+               uint32_t group, uint32_t flags, const void *d_x, uint64_t ldx, uint64_t tokens,
+               void *d_y, uint64_t ldy, int32_t *d_status, void *stream);
+int wc_q4_gemm_experts(const void *d_streams, uint64_t stream_stride, uint32_t experts,
+                       uint64_t rows, uint64_t cols, uint32_t group, uint32_t flags,
+                       const void *d_x, uint64_t ldx, uint64_t tokens, const int32_t *d_offsets,
+                       void *d_y, uint64_t ldy, int32_t *d_status, void *stream);
+
+/*
+ * Rows sorted by expert and back: what stands around the products of a layer
+ * of experts (wc_q4_gemm_experts, or wc_gemm on the rows of one expert). A slot
+ * is one (token, choice) pair, tokens x top of them in row-major order.
+ *
+ *  wc_moe_sort       from each slot's expert id: d_offsets[e] = first sorted row
+ *                    of expert e (experts + 1 values, the last one the number
+ *                    of sorted rows), d_inverse[slot] = the slot's sorted row,
+ *                    and (may be NULL) d_order[row] = its slot. Stable: within
+ *                    an expert, slots keep their order. A slot whose id is
+ *                    outside 0..experts-1 is dropped: inverse -1; d_order
+ *                    (slots values) is -1 behind the last sorted row.
+ *  wc_moe_gather     rows[inverse[t, j]] = x[t]; rows that no slot names are
+ *                    left as they were
+ *  wc_moe_combine    out[t] = sum_j weights[t, j] * rows[inverse[t, j]] over the
+ *                    slots that have a row (none: 0), summed in FP32 in the
+ *                    order of j, rounded once. weights NULL: all 1, which is
+ *                    the gradient of wc_moe_gather (rows = the gradient of its
+ *                    result, out = the gradient of x).
+ *  wc_moe_combine_backward  the gradients of wc_moe_combine:
+ *                    drows[inverse[t, j]] = weights[t, j] * dout[t] (one
+ *                    rounding; rows that no slot names are left as they were)
+ *                    and (may be NULL) dweights[t, j] = <dout[t], rows[...]> in
+ *                    FP32 in a fixed order, 0 for a slot without a row
+ * x, rows, out, dout and drows have elements of `dtype`, aligned to it, rows ld
+ * elements apart; `rows` counts the rows of the sorted matrices, and an inverse
+ * outside 0..rows-1 means that the slot has none. A row may be named by one slot
+ * only in wc_moe_gather and wc_moe_combine_backward (as wc_moe_sort leaves it;
+ * otherwise which of the slots writes it is unspecified). Every result is the
+ * same on every run. No workspace.
+ */
+int wc_moe_sort(const int32_t *d_ids, uint64_t slots, uint32_t experts, int32_t *d_offsets,
+                int32_t *d_order, int32_t *d_inverse, void *stream);
+int wc_moe_gather(const void *d_x, uint64_t ldx, uint64_t tokens, uint64_t top, uint64_t cols,
+                  uint32_t dtype, const int32_t *d_inverse, void *d_rows, uint64_t ldr,
+                  uint64_t rows, void *stream);
+int wc_moe_combine(const void *d_rows, uint64_t ldr, uint64_t rows, uint64_t tokens, uint64_t top,
+                   uint64_t cols, uint32_t dtype, const int32_t *d_inverse, const float *d_weights,
+                   void *d_out, uint64_t ldo, void *stream);
+int wc_moe_combine_backward(const void *d_dout, uint64_t ldd, const void *d_rows, uint64_t ldr,
+                            uint64_t rows, uint64_t tokens, uint64_t top, uint64_t cols,
+                            uint32_t dtype, const int32_t *d_inverse, const float *d_weights,
+                            void *d_drows, uint64_t lddr, float *d_dweights, void *stream);
+
+/*
  * Parse a host copy of a stream's first `header_bytes` (>= 128) bytes. Fills
  * n, block and total_bytes (any may be NULL). Returns WC_ERR_CORRUPT_STREAM
  * if the header is not a WCB1 version-1 header consistent with itself (BF16,
- * FP32, escape-coded or tANS-coded stream; header bytes 12..15 say which; for
- * a tANS-coded stream `block` is its chunk size).
+ * FP32, escape-coded, tANS-coded or 4-bit stream; header bytes 12..15 say
+ * which; for a tANS-coded stream `block` is its chunk size, for a 4-bit stream
+ * its group).
  */
 int wc_stream_info(const void *h_header, uint64_t header_bytes,
                    uint64_t *n, uint32_t *block, uint64_t *total_bytes);

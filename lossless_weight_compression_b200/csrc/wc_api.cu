@@ -6,6 +6,7 @@
 
 #include "../../include/wcodec.h"
 #include "wc_internal.cuh"
+#include "wc_q4_core.cuh"
 
 namespace {
 
@@ -666,6 +667,21 @@ int wc_stream_info(const void* h_header, uint64_t header_bytes, uint64_t* n, uin
         if (n) *n = nn;
         if (block) *block = B;
         if (total_bytes) *total_bytes = total;
+        return WC_OK;
+    }
+    if ((flags & ~uint64_t(wc::kFlagQ4Zeros | wc::kFlagQ4Half)) == wc::kFlagQ4) {
+        const uint64_t rows = get_le(p + 88, 4), cols = get_le(p + 92, 4);
+        if (!wc::q4_group_ok(B) || rows > WC_Q4_MAX_ROWS || cols < 1 || cols > WC_Q4_MAX_COLS)
+            return WC_ERR_CORRUPT_STREAM;
+        const wc::Q4Layout L =
+            wc::q4_layout(uint32_t(rows), uint32_t(cols), B,
+                          (flags & wc::kFlagQ4Zeros ? wc::kQ4Zeros : 0u) |
+                              (flags & wc::kFlagQ4Half ? wc::kQ4ScalesHalf : 0u));
+        for (int k = 0; k < 16; ++k)
+            if (get_le(p + 8 * k, 8) != wc::q4_header_word(L, k)) return WC_ERR_CORRUPT_STREAM;
+        if (n) *n = nn;
+        if (block) *block = B;
+        if (total_bytes) *total_bytes = L.total;
         return WC_OK;
     }
     if (flags > 2 || !args_ok(nn, B)) return WC_ERR_CORRUPT_STREAM;

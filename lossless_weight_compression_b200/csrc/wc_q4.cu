@@ -1,0 +1,267 @@
+// wc_q4.cu -- 4-bit streams with group scales: quantizing a 16-bit matrix,
+// packing given codes, and expanding a stream (sm_100a).
+//
+// One thread block of 8 warps per 128 rows x 128 columns, one warp per record
+// of 16 rows: lane l holds columns 8 (l & 15) .. + 7 of row l >> 4 of a row
+// pair, so a group of 32, 64 or 128 columns is 4, 8 or 16 neighbouring lanes
+// and its range is reduced by shuffles; the eight records are put together in
+// shared memory and leave as one contiguous run of 16-byte stores. Each weight
+// is read once and each stream byte written once: bound by memory traffic.
+#include "wc_q4_core.cuh"
+
+namespace wc {
+namespace {
+
+constexpr int kQ4Threads = 256;
+constexpr uint32_t kMaxRec = kQ4Codes + 32u * 4u + 64u;  // group 32 with zero points
+
+template <bool HALF>
+__device__ __forceinline__ float to_float(uint16_t b) {
+    return HALF ? __half2float(__ushort_as_half(b)) : __uint_as_float(uint32_t(b) << 16);
+}
+
+template <bool HALF>
+__device__ __forceinline__ uint16_t from_float(float v) {
+    return HALF ? __half_as_ushort(__float2half_rn(v)) : __bfloat16_as_ushort(__float2bfloat16_rn(v));
+}
+
+// Eight consecutive 16-bit values of a row from column c, zeros past the end.
+__device__ __forceinline__ uint4 load8(const uint16_t* row, uint32_t c, uint32_t cols, bool live,
+                                       bool vec) {
+    if (!live || c >= cols) return make_uint4(0, 0, 0, 0);
+    if (vec && c + 8 <= cols) return ld_stream_v4(row + c);
+    uint32_t v[4] = {0, 0, 0, 0};
+#pragma unroll
+    for (uint32_t k = 0; k < 8; ++k)
+        if (c + k < cols) v[k >> 1] |= uint32_t(row[c + k]) << (16 * (k & 1));
+    return make_uint4(v[0], v[1], v[2], v[3]);
+}
+
+// The word of eight codes in element order.
+__device__ __forceinline__ uint32_t pack8(const uint32_t (&q)[8]) {
+    uint32_t w = 0;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) w |= q[e] << (4 * ((e >> 1) + 4 * (e & 1)));
+    return w;
+}
+
+// The block's records from shared memory to the stream.
+__device__ __forceinline__ void store_records(uint8_t* dst, const uint8_t* sm, uint32_t bytes) {
+    __syncthreads();
+    for (uint32_t k = threadIdx.x * 16u; k < bytes; k += kQ4Threads * 16u)
+        *reinterpret_cast<uint4*>(dst + k) = *reinterpret_cast<const uint4*>(sm + k);
+}
+
+__device__ __forceinline__ void store_header(const Q4Layout& L, uint8_t* out) {
+    if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x < 16)
+        reinterpret_cast<uint64_t*>(out)[threadIdx.x] = q4_header_word(L, threadIdx.x);
+}
+
+// Scale, zero point and codes of each group, round to nearest even throughout:
+//   without zero points  s = rnd16(max|w| / 7), q = clamp(rint(w / s), -8, 7) + 8
+//   with zero points     lo = min(w, 0), hi = max(w, 0), s = rnd16((hi - lo) / 15),
+//                        z = clamp(rint(-lo / s), 0, 15), q = clamp(rint(w / s) + z, 0, 15)
+// (s = 0: every code stands for zero). The quotients are FP32 with one rounding;
+// w and s have at most 11 significant bits, so no quotient that is not a tie in
+// exact arithmetic comes within an FP32 rounding of one.
+template <bool HALF>
+__global__ void __launch_bounds__(kQ4Threads)
+    q4_quantize_kernel(const uint16_t* __restrict__ w, uint64_t ld, Q4Layout L, bool vec,
+                       uint8_t* __restrict__ out) {
+    extern __shared__ __align__(16) uint8_t sm[];
+    const uint32_t lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const uint32_t b0 = blockIdx.y * 8, s = blockIdx.x;
+    const uint32_t h = min(8u, L.blocks16 - b0);
+    store_header(L, out);
+    if (warp < h) {
+        uint8_t* rec = sm + warp * L.rec;
+        const uint32_t c8 = lane & 15u, c = s * kQ4Cols + 8 * c8;
+        uint4 v[8];
+#pragma unroll
+        for (uint32_t k = 0; k < 8; ++k) {
+            const uint32_t row = (b0 + warp) * kQ4Rows + 2 * k + (lane >> 4);
+            v[k] = load8(w + uint64_t(row) * ld, c, L.cols, row < L.rows, vec);
+        }
+#pragma unroll
+        for (uint32_t k = 0; k < 8; ++k) {
+            const uint32_t r = 2 * k + (lane >> 4);
+            float f[8];
+            const uint32_t u[4] = {v[k].x, v[k].y, v[k].z, v[k].w};
+#pragma unroll
+            for (int e = 0; e < 8; ++e) f[e] = to_float<HALF>(uint16_t(u[e >> 1] >> (16 * (e & 1))));
+            // NaN has to reach the scale, which fminf and fmaxf would drop
+            float lo = 0.f, hi = 0.f, nan = 0.f;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                lo = fminf(lo, f[e]);
+                hi = fmaxf(hi, f[e]);
+                nan += f[e] != f[e] ? 1.f : 0.f;
+            }
+            for (uint32_t o = 1; o < L.group / 8; o *= 2) {
+                lo = fminf(lo, __shfl_xor_sync(0xFFFFFFFFu, lo, o));
+                hi = fmaxf(hi, __shfl_xor_sync(0xFFFFFFFFu, hi, o));
+                nan += __shfl_xor_sync(0xFFFFFFFFu, nan, o);
+            }
+            const float range = L.zeros ? (hi - lo) / 15.f : fmaxf(hi, -lo) / 7.f;
+            const uint16_t sbits = from_float<HALF>(nan > 0.f ? __int_as_float(0x7FC00000) : range);
+            const float sc = to_float<HALF>(sbits);
+            const float d = sc > 0.f ? sc : 1.f;
+            const float z = L.zeros ? fminf(fmaxf(rintf(-lo / d), 0.f), 15.f) : 8.f;
+            uint32_t q[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                q[e] = uint32_t(fminf(fmaxf(rintf(f[e] / d) + z, 0.f), 15.f));
+            const uint32_t i = c8 >> 2, t = c8 & 3u;
+            *reinterpret_cast<uint32_t*>(rec + t * 256 + r * 16 + i * 4) = pack8(q);
+            if ((c8 & (L.group / 8 - 1)) == 0) {
+                const uint32_t g = c8 / (L.group / 8);
+                *reinterpret_cast<uint16_t*>(rec + kQ4Codes + (g * 16 + r) * 2) = sbits;
+                if (L.zeros) rec[kQ4Codes + 32 * L.per + g * 16 + r] = uint8_t(z);
+            }
+        }
+        if (L.zeros && L.per == 1 && lane < 16) rec[kQ4Codes + 32 + 16 + lane] = 0;  // padding
+    }
+    store_records(out + q4_record(L, b0, s), sm, h * L.rec);
+}
+
+__global__ void __launch_bounds__(kQ4Threads)
+    q4_pack_kernel(const uint8_t* __restrict__ codes, const uint16_t* __restrict__ scales,
+                   const uint8_t* __restrict__ zeros, Q4Layout L, uint8_t* __restrict__ out) {
+    extern __shared__ __align__(16) uint8_t sm[];
+    const uint32_t lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const uint32_t b0 = blockIdx.y * 8, s = blockIdx.x;
+    const uint32_t h = min(8u, L.blocks16 - b0);
+    const uint32_t groups = uint32_t((uint64_t(L.cols) + L.group - 1) / L.group);
+    store_header(L, out);
+    if (warp < h) {
+        uint8_t* rec = sm + warp * L.rec;
+        const uint32_t c8 = lane & 15u, c = s * kQ4Cols + 8 * c8;
+        const uint32_t g = c8 / (L.group / 8), gg = s * L.per + g;
+        for (uint32_t k = 0; k < 8; ++k) {
+            const uint32_t r = 2 * k + (lane >> 4), row = (b0 + warp) * kQ4Rows + r;
+            const bool live = row < L.rows;
+            const bool has = live && gg < groups;
+            const uint32_t z = !L.zeros ? 8u : has ? zeros[uint64_t(row) * groups + gg] & 15u : 0u;
+            uint32_t q[8];
+#pragma unroll
+            for (uint32_t e = 0; e < 8; ++e)
+                q[e] = live && c + e < L.cols ? codes[uint64_t(row) * L.cols + c + e] & 15u : z;
+            *reinterpret_cast<uint32_t*>(rec + (c8 & 3u) * 256 + r * 16 + (c8 >> 2) * 4) = pack8(q);
+            if ((c8 & (L.group / 8 - 1)) == 0) {
+                *reinterpret_cast<uint16_t*>(rec + kQ4Codes + (g * 16 + r) * 2) =
+                    has ? scales[uint64_t(row) * groups + gg] : uint16_t(0);
+                if (L.zeros) rec[kQ4Codes + 32 * L.per + g * 16 + r] = uint8_t(z);
+            }
+        }
+        if (L.zeros && L.per == 1 && lane < 16) rec[kQ4Codes + 32 + 16 + lane] = 0;  // padding
+    }
+    store_records(out + q4_record(L, b0, s), sm, h * L.rec);
+}
+
+// s (q - z) in FP32 is exact (at most 11 + 4 bits); one rounding to 16 bits.
+template <int DT>
+__global__ void __launch_bounds__(kQ4Threads)
+    q4_dequantize_kernel(const uint8_t* __restrict__ in, Q4Layout L, void* __restrict__ out,
+                         uint64_t ld, bool vec, int32_t* status) {
+    extern __shared__ __align__(16) uint8_t sm[];
+    const uint32_t lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const uint32_t b0 = blockIdx.y * 8, s = blockIdx.x;
+    const uint32_t h = min(8u, L.blocks16 - b0);
+    if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) q4_check_header(in, L, status);
+    const uint8_t* src = in + q4_record(L, b0, s);
+    for (uint32_t k = threadIdx.x * 16u; k < h * L.rec; k += kQ4Threads * 16u)
+        *reinterpret_cast<uint4*>(sm + k) = ld_stream_v4(src + k);
+    __syncthreads();
+    if (warp >= h) return;
+    const uint8_t* rec = sm + warp * L.rec;
+    const uint32_t c8 = lane & 15u, c = s * kQ4Cols + 8 * c8;
+    const uint32_t g = c8 / (L.group / 8);
+    if (c >= L.cols) return;
+#pragma unroll
+    for (uint32_t k = 0; k < 8; ++k) {
+        const uint32_t r = 2 * k + (lane >> 4), row = (b0 + warp) * kQ4Rows + r;
+        if (row >= L.rows) continue;
+        const uint32_t word =
+            *reinterpret_cast<const uint32_t*>(rec + (c8 & 3u) * 256 + r * 16 + (c8 >> 2) * 4);
+        const float sc = q4_scale(*reinterpret_cast<const uint16_t*>(rec + kQ4Codes + (g * 16 + r) * 2),
+                                  L.half_scales);
+        const int z = L.zeros ? int(rec[kQ4Codes + 32 * L.per + g * 16 + r] & 15u) : 8;
+        float f[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            f[e] = sc * float(int((word >> (4 * ((e >> 1) + 4 * (e & 1)))) & 15u) - z);
+        if (DT == 2) {
+            float* o = static_cast<float*>(out) + uint64_t(row) * ld + c;
+            if (vec && c + 8 <= L.cols) {
+                st_stream_v4(o, make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]),
+                                           __float_as_uint(f[2]), __float_as_uint(f[3])));
+                st_stream_v4(o + 4, make_uint4(__float_as_uint(f[4]), __float_as_uint(f[5]),
+                                               __float_as_uint(f[6]), __float_as_uint(f[7])));
+            } else {
+#pragma unroll
+                for (uint32_t e = 0; e < 8; ++e)
+                    if (c + e < L.cols) o[e] = f[e];
+            }
+        } else {
+            uint16_t* o = static_cast<uint16_t*>(out) + uint64_t(row) * ld + c;
+            uint16_t b[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) b[e] = from_float<DT == 1>(f[e]);
+            if (vec && c + 8 <= L.cols) {
+                st_stream_v4(o, make_uint4(b[0] | uint32_t(b[1]) << 16, b[2] | uint32_t(b[3]) << 16,
+                                           b[4] | uint32_t(b[5]) << 16, b[6] | uint32_t(b[7]) << 16));
+            } else {
+#pragma unroll
+                for (uint32_t e = 0; e < 8; ++e)
+                    if (c + e < L.cols) o[e] = b[e];
+            }
+        }
+    }
+}
+
+bool vec_ok(const void* p, uint64_t ld, uint32_t size) {
+    return (reinterpret_cast<uintptr_t>(p) & 15u) == 0 && (ld * size) % 16u == 0;
+}
+
+dim3 q4_grid(const Q4Layout& L) { return dim3(L.slices, (L.blocks16 + 7) / 8); }
+
+// An empty matrix is a bare header.
+__global__ void q4_header_kernel(Q4Layout L, uint8_t* out) { store_header(L, out); }
+
+}  // namespace
+
+cudaError_t launch_q4_quantize(const void* w, uint64_t ld, const Q4Layout& L, uint8_t* out,
+                               cudaStream_t stream) {
+    if (L.blocks16 == 0) {
+        q4_header_kernel<<<1, 32, 0, stream>>>(L, out);
+        return cudaGetLastError();
+    }
+    const auto kernel = L.half_scales ? q4_quantize_kernel<true> : q4_quantize_kernel<false>;
+    kernel<<<q4_grid(L), kQ4Threads, 8 * kMaxRec, stream>>>(static_cast<const uint16_t*>(w), ld, L,
+                                                            vec_ok(w, ld, 2), out);
+    return cudaGetLastError();
+}
+
+cudaError_t launch_q4_pack(const uint8_t* codes, const void* scales, const uint8_t* zeros,
+                           const Q4Layout& L, uint8_t* out, cudaStream_t stream) {
+    if (L.blocks16 == 0) {
+        q4_header_kernel<<<1, 32, 0, stream>>>(L, out);
+        return cudaGetLastError();
+    }
+    q4_pack_kernel<<<q4_grid(L), kQ4Threads, 8 * kMaxRec, stream>>>(
+        codes, static_cast<const uint16_t*>(scales), zeros, L, out);
+    return cudaGetLastError();
+}
+
+cudaError_t launch_q4_dequantize(const uint8_t* in, const Q4Layout& L, void* out, uint64_t ld,
+                                 uint32_t dtype, int32_t* status, cudaStream_t stream) {
+    if (L.blocks16 == 0) return cudaSuccess;
+    const auto kernel = dtype == 2   ? q4_dequantize_kernel<2>
+                        : dtype == 1 ? q4_dequantize_kernel<1>
+                                     : q4_dequantize_kernel<0>;
+    kernel<<<q4_grid(L), kQ4Threads, 8 * kMaxRec, stream>>>(in, L, out, ld,
+                                                            vec_ok(out, ld, dtype == 2 ? 4 : 2), status);
+    return cudaGetLastError();
+}
+
+}  // namespace wc

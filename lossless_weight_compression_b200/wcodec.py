@@ -149,6 +149,26 @@ def lib() -> ctypes.CDLL:
     L.wc_decompress_host.restype = i
     L.wc_decompress_host_batch.argtypes = [ctypes.POINTER(wc_batch_item), u32, u32, vp, vp]
     L.wc_decompress_host_batch.restype = i
+    L.wc_q4_bytes.argtypes, L.wc_q4_bytes.restype = [u64, u64, u32, u32], u64
+    L.wc_q4_quantize.argtypes = [vp, u64, u64, u64, u32, u32, vp, u64, vp]
+    L.wc_q4_quantize.restype = i
+    L.wc_q4_pack.argtypes = [vp, vp, vp, u64, u64, u32, u32, vp, u64, vp]
+    L.wc_q4_pack.restype = i
+    L.wc_q4_dequantize.argtypes = [vp, u64, u64, u64, u32, u32, vp, u64, u32, vp, vp]
+    L.wc_q4_dequantize.restype = i
+    L.wc_q4_gemm.argtypes = [vp, u64, u64, u64, u32, u32, vp, u64, u64, vp, u64, vp, vp]
+    L.wc_q4_gemm.restype = i
+    L.wc_q4_gemm_experts.argtypes = [vp, u64, u32, u64, u64, u32, u32, vp, u64, u64, vp, vp, u64,
+                                     vp, vp]
+    L.wc_q4_gemm_experts.restype = i
+    L.wc_moe_sort.argtypes, L.wc_moe_sort.restype = [vp, u64, u32, vp, vp, vp, vp], i
+    L.wc_moe_gather.argtypes = [vp, u64, u64, u64, u64, u32, vp, vp, u64, u64, vp]
+    L.wc_moe_gather.restype = i
+    L.wc_moe_combine.argtypes = [vp, u64, u64, u64, u64, u64, u32, vp, vp, vp, u64, vp]
+    L.wc_moe_combine.restype = i
+    L.wc_moe_combine_backward.argtypes = [vp, u64, vp, u64, u64, u64, u64, u64, u32, vp, vp, vp, u64,
+                                          vp, vp]
+    L.wc_moe_combine_backward.restype = i
     _lib = L
     return L
 
@@ -297,6 +317,67 @@ def wc_decompress_host(h_stream, stream_bytes, d_out, n, block, flags, d_status,
 
 def wc_decompress_host_batch(items, count, flags, d_status, stream) -> int:
     return lib().wc_decompress_host_batch(items, count, flags, d_status, stream)
+
+
+WC_Q4_ZEROS = 1
+WC_Q4_SCALES_FP16 = 2
+WC_Q4_X_FP16 = 4
+WC_Q4_Y_16BIT = 8
+WC_DTYPE_BF16, WC_DTYPE_FP16, WC_DTYPE_FP32 = 0, 1, 2
+WC_MOE_MAX_EXPERTS = 1024
+
+
+def wc_q4_bytes(rows, cols, group, flags) -> int:
+    return lib().wc_q4_bytes(rows, cols, group, flags)
+
+
+def wc_q4_quantize(d_w, ld, rows, cols, group, flags, d_out, out_capacity, stream) -> int:
+    return lib().wc_q4_quantize(d_w, ld, rows, cols, group, flags, d_out, out_capacity, stream)
+
+
+def wc_q4_pack(d_codes, d_scales, d_zeros, rows, cols, group, flags, d_out, out_capacity,
+               stream) -> int:
+    return lib().wc_q4_pack(d_codes, d_scales, d_zeros, rows, cols, group, flags, d_out,
+                            out_capacity, stream)
+
+
+def wc_q4_dequantize(d_stream, stream_bytes, rows, cols, group, flags, d_out, ld, dtype, d_status,
+                     stream) -> int:
+    return lib().wc_q4_dequantize(d_stream, stream_bytes, rows, cols, group, flags, d_out, ld,
+                                  dtype, d_status, stream)
+
+
+def wc_q4_gemm(d_stream, stream_bytes, rows, cols, group, flags, d_x, ldx, tokens, d_y, ldy,
+               d_status, stream) -> int:
+    return lib().wc_q4_gemm(d_stream, stream_bytes, rows, cols, group, flags, d_x, ldx, tokens, d_y,
+                            ldy, d_status, stream)
+
+
+def wc_q4_gemm_experts(d_streams, stream_stride, experts, rows, cols, group, flags, d_x, ldx,
+                       tokens, d_offsets, d_y, ldy, d_status, stream) -> int:
+    return lib().wc_q4_gemm_experts(d_streams, stream_stride, experts, rows, cols, group, flags,
+                                    d_x, ldx, tokens, d_offsets, d_y, ldy, d_status, stream)
+
+
+def wc_moe_sort(d_ids, slots, experts, d_offsets, d_order, d_inverse, stream) -> int:
+    return lib().wc_moe_sort(d_ids, slots, experts, d_offsets, d_order, d_inverse, stream)
+
+
+def wc_moe_gather(d_x, ldx, tokens, top, cols, dtype, d_inverse, d_rows, ldr, rows, stream) -> int:
+    return lib().wc_moe_gather(d_x, ldx, tokens, top, cols, dtype, d_inverse, d_rows, ldr, rows,
+                               stream)
+
+
+def wc_moe_combine(d_rows, ldr, rows, tokens, top, cols, dtype, d_inverse, d_weights, d_out, ldo,
+                   stream) -> int:
+    return lib().wc_moe_combine(d_rows, ldr, rows, tokens, top, cols, dtype, d_inverse, d_weights,
+                                d_out, ldo, stream)
+
+
+def wc_moe_combine_backward(d_dout, ldd, d_rows, ldr, rows, tokens, top, cols, dtype, d_inverse,
+                            d_weights, d_drows, lddr, d_dweights, stream) -> int:
+    return lib().wc_moe_combine_backward(d_dout, ldd, d_rows, ldr, rows, tokens, top, cols, dtype,
+                                         d_inverse, d_weights, d_drows, lddr, d_dweights, stream)
 
 
 def wc_stream_info(h_header: bytes):
@@ -693,3 +774,337 @@ def decompress_tans(stream_bytes: torch.Tensor, n: int, chunk: int, *,
                             chunk, status.data_ptr(), _stream_handle(stream))
     _check(rc, "wc_decompress_tans")
     return out
+
+
+# ---------------------------------------------------------------------------
+# 4-bit streams with group scales, their products, and the expert routing. These
+# run on the tensors' device and, unless `stream` is given, on its current
+# stream; results are allocated on the stream that the work runs on.
+# ---------------------------------------------------------------------------
+_DTYPES = {torch.bfloat16: WC_DTYPE_BF16, torch.float16: WC_DTYPE_FP16,
+           torch.float32: WC_DTYPE_FP32}
+
+
+def _run_on(device: torch.device, stream, fn):
+    """fn(stream handle) with `device` current and `stream` (default: the
+    device's current stream) the one that tensors are allocated on."""
+    if device.type != "cuda":
+        raise ValueError("wcodec works on CUDA tensors; got one on %s" % device)
+    if stream is None and device.index == torch.cuda.current_device():
+        return fn(torch.cuda.current_stream().cuda_stream)
+    with torch.cuda.device(device):
+        if stream is None:
+            return fn(torch.cuda.current_stream().cuda_stream)
+        with torch.cuda.stream(stream):
+            return fn(stream.cuda_stream)
+
+
+def _rows(t: torch.Tensor, cols: int, what: str, device=None) -> torch.Tensor:
+    """A matrix of `cols` columns whose rows are dense (they may lie apart)."""
+    if t.dim() != 2 or t.shape[1] != cols:
+        raise ValueError("%s must be a matrix of %d columns; got %s" % (what, cols, tuple(t.shape)))
+    if device is not None and t.device != device:
+        raise ValueError("%s is on %s, not on %s" % (what, t.device, device))
+    if t.numel() and ((cols > 1 and t.stride(1) != 1)
+                      or (t.shape[0] > 1 and t.stride(0) < cols)):
+        raise ValueError("%s must have dense rows; got strides %s" % (what, t.stride()))
+    return t
+
+
+def _ld(t: torch.Tensor) -> int:
+    """Elements between rows (the stride of a single row or of none means nothing)."""
+    return t.stride(0) if t.shape[0] > 1 and t.numel() else t.shape[1]
+
+
+def _vector(t: torch.Tensor, shape: tuple, dtype: torch.dtype, what: str, device) -> torch.Tensor:
+    if tuple(t.shape) != shape or t.dtype != dtype or t.device != device or not t.is_contiguous():
+        raise ValueError("%s must be a contiguous %s tensor of shape %s on %s"
+                         % (what, dtype, shape, device))
+    return t
+
+
+@dataclass
+class Q4Matrix:
+    """A rows x cols matrix held as a 4-bit stream: ``buffer`` is its bytes
+    (uint8), or (experts, bytes) for the matrices of several experts."""
+    buffer: torch.Tensor
+    rows: int
+    cols: int
+    group: int
+    zeros: bool
+    scale_dtype: torch.dtype
+
+    def flags(self) -> int:
+        if self.scale_dtype not in (torch.bfloat16, torch.float16):
+            raise TypeError("scales are BF16 or FP16; got %s" % self.scale_dtype)
+        return (WC_Q4_ZEROS if self.zeros else 0) | (
+            WC_Q4_SCALES_FP16 if self.scale_dtype == torch.float16 else 0)
+
+
+def _q4_buffer(m: Q4Matrix, dims: int) -> torch.Tensor:
+    b = m.buffer
+    if b.dtype != torch.uint8 or b.dim() != dims or (b.shape[-1] > 1 and b.stride(-1) != 1):
+        raise ValueError("a 4-bit stream is a dense uint8 tensor of %d dimension(s); got %s %s"
+                         % (dims, b.dtype, tuple(b.shape)))
+    return b
+
+
+def _q4_size(rows: int, cols: int, group: int, flags: int) -> int:
+    size = wc_q4_bytes(rows, cols, group, flags) if rows >= 0 and cols >= 0 else 0
+    if size == 0:
+        raise WcodecError(WC_ERR_INVALID_ARG, "4-bit stream of %r x %r in groups of %r"
+                          % (rows, cols, group))
+    return size
+
+
+def quantize_q4(w: torch.Tensor, group: int = 128, *, zeros: bool = False,
+                out: torch.Tensor | None = None, stream=None) -> Q4Matrix:
+    """Round a BF16 or FP16 matrix to a 4-bit stream with one scale of its type
+    (and with ``zeros`` a zero point) per row and ``group`` columns."""
+    if w.dtype not in (torch.bfloat16, torch.float16):
+        raise TypeError("quantize_q4 takes BF16 or FP16; got %s" % w.dtype)
+    rows, cols = _rows(w, w.shape[-1], "w").shape
+    m = Q4Matrix(out, rows, cols, group, zeros, w.dtype)
+    flags = m.flags()
+    size = _q4_size(rows, cols, group, flags)
+
+    def run(handle):
+        if m.buffer is None:
+            m.buffer = torch.empty(size, dtype=torch.uint8, device=w.device)
+        elif m.buffer.device != w.device:
+            raise ValueError("out is on %s, not on %s" % (m.buffer.device, w.device))
+        b = _q4_buffer(m, 1)
+        _check(wc_q4_quantize(w.data_ptr(), _ld(w), rows, cols, group, flags, b.data_ptr(),
+                              b.numel(), handle), "wc_q4_quantize")
+        return m
+    return _run_on(w.device, stream, run)
+
+
+def pack_q4(codes: torch.Tensor, scales: torch.Tensor, zeros: torch.Tensor | None = None, *,
+            group: int = 128, out: torch.Tensor | None = None, stream=None) -> Q4Matrix:
+    """The stream of given codes (uint8, rows x cols, 0..15), scales (BF16 or
+    FP16, rows x ceil(cols / group)) and zero points (uint8, as the scales)."""
+    if codes.dim() != 2 or codes.device.type != "cuda":
+        raise ValueError("codes must be a CUDA matrix")
+    rows, cols = codes.shape
+    m = Q4Matrix(out, rows, cols, group, zeros is not None, scales.dtype)
+    flags = m.flags()
+    size = _q4_size(rows, cols, group, flags)
+    shape = (rows, -(-cols // group))
+    _vector(codes, (rows, cols), torch.uint8, "codes", codes.device)
+    _vector(scales, shape, scales.dtype, "scales", codes.device)
+    if zeros is not None:
+        _vector(zeros, shape, torch.uint8, "zeros", codes.device)
+
+    def run(handle):
+        if m.buffer is None:
+            m.buffer = torch.empty(size, dtype=torch.uint8, device=codes.device)
+        elif m.buffer.device != codes.device:
+            raise ValueError("out is on %s, not on %s" % (m.buffer.device, codes.device))
+        b = _q4_buffer(m, 1)
+        _check(wc_q4_pack(codes.data_ptr(), scales.data_ptr(),
+                          None if zeros is None else zeros.data_ptr(), rows, cols, group, flags,
+                          b.data_ptr(), b.numel(), handle), "wc_q4_pack")
+        return m
+    return _run_on(codes.device, stream, run)
+
+
+def dequantize_q4(m: Q4Matrix, dtype: torch.dtype = torch.bfloat16, *,
+                  out: torch.Tensor | None = None, status: torch.Tensor | None = None,
+                  stream=None) -> torch.Tensor:
+    """The weights of a 4-bit stream, rounded once to ``dtype`` (BF16, FP16 or FP32)."""
+    b = _q4_buffer(m, 1)
+    if out is not None:
+        dtype = _rows(out, m.cols, "out", b.device).dtype
+        if out.shape[0] != m.rows:
+            raise ValueError("out must have %d rows" % m.rows)
+    if dtype not in _DTYPES:
+        raise TypeError("dequantize_q4 gives BF16, FP16 or FP32; got %s" % dtype)
+
+    def run(handle):
+        o = torch.empty((m.rows, m.cols), dtype=dtype, device=b.device) if out is None else out
+        _check(wc_q4_dequantize(b.data_ptr(), b.numel(), m.rows, m.cols, m.group, m.flags(),
+                                o.data_ptr(), _ld(o), _DTYPES[dtype],
+                                None if status is None else status.data_ptr(), handle),
+               "wc_q4_dequantize")
+        return o
+    return _run_on(b.device, stream, run)
+
+
+def _q4_product(m: Q4Matrix, b, x, offsets, y, out_dtype, status, stream):
+    if x.dtype not in (torch.bfloat16, torch.float16):
+        raise TypeError("activations are BF16 or FP16; got %s" % x.dtype)
+    _rows(x, m.cols, "x", b.device)
+    tokens = x.shape[0]
+    if y is not None:
+        out_dtype = _rows(y, m.rows, "y", b.device).dtype
+        if y.shape[0] != tokens:
+            raise ValueError("y must have %d rows" % tokens)
+    if out_dtype != torch.float32 and out_dtype != x.dtype:
+        raise TypeError("the product is FP32 or has x's type; got %s" % out_dtype)
+    flags = m.flags() | (WC_Q4_X_FP16 if x.dtype == torch.float16 else 0) | (
+        0 if out_dtype == torch.float32 else WC_Q4_Y_16BIT)
+
+    def run(handle):
+        o = torch.empty((tokens, m.rows), dtype=out_dtype, device=b.device) if y is None else y
+        st = None if status is None else status.data_ptr()
+        if offsets is None:
+            rc = lib().wc_q4_gemm(b.data_ptr(), b.numel(), m.rows, m.cols, m.group, flags,
+                                  x.data_ptr(), _ld(x), tokens, o.data_ptr(), _ld(o), st, handle)
+            _check(rc, "wc_q4_gemm")
+        else:
+            rc = lib().wc_q4_gemm_experts(b.data_ptr(),
+                                          b.stride(0) if b.shape[0] > 1 else b.shape[1],
+                                          b.shape[0], m.rows, m.cols, m.group, flags, x.data_ptr(),
+                                          _ld(x), tokens, offsets.data_ptr(), o.data_ptr(), _ld(o),
+                                          st, handle)
+            _check(rc, "wc_q4_gemm_experts")
+        return o
+    return _run_on(b.device, stream, run)
+
+
+def gemm_q4(m: Q4Matrix, x: torch.Tensor, *, y: torch.Tensor | None = None,
+            out_dtype: torch.dtype = torch.float32, status: torch.Tensor | None = None,
+            stream=None) -> torch.Tensor:
+    """y = x @ W.T with W held as a 4-bit stream; x is (tokens, cols) BF16 or
+    FP16, y (tokens, rows) in FP32 or x's type."""
+    return _q4_product(m, _q4_buffer(m, 1), x, None, y, out_dtype, status, stream)
+
+
+def gemm_q4_experts(m: Q4Matrix, x: torch.Tensor, offsets: torch.Tensor, *,
+                    y: torch.Tensor | None = None, out_dtype: torch.dtype = torch.float32,
+                    status: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """gemm_q4 over the matrices of m.buffer's experts: rows offsets[e] ..
+    offsets[e + 1] - 1 of x take matrix e (offsets int32, as moe_sort gives
+    them). Rows outside every range are left as they were in ``y``."""
+    b = _q4_buffer(m, 2)
+    _vector(offsets, (b.shape[0] + 1,), torch.int32, "offsets", b.device)
+    return _q4_product(m, b, x, offsets, y, out_dtype, status, stream)
+
+
+@dataclass
+class MoePlan:
+    """Where each (token, choice) slot's row lies among the rows sorted by
+    expert: offsets (experts + 1), order (slot of each sorted row, -1 behind
+    them; may be None), inverse ((tokens, top), -1: dropped); all int32."""
+    offsets: torch.Tensor
+    order: torch.Tensor | None
+    inverse: torch.Tensor
+
+
+def moe_sort(ids: torch.Tensor, experts: int, *, stream=None) -> MoePlan:
+    """The plan that sorts (token, choice) slots by expert: ids is (tokens, top)
+    int32; ids outside 0..experts-1 are dropped."""
+    if ids.dim() != 2:
+        raise ValueError("ids must be (tokens, top)")
+    _vector(ids, tuple(ids.shape), torch.int32, "ids", ids.device)
+    if not 1 <= experts <= WC_MOE_MAX_EXPERTS:
+        raise ValueError("1 to %d experts; got %r" % (WC_MOE_MAX_EXPERTS, experts))
+
+    def run(handle):
+        slots = ids.numel()
+        offsets = torch.empty(experts + 1, dtype=torch.int32, device=ids.device)
+        order = torch.empty(slots, dtype=torch.int32, device=ids.device)
+        inverse = torch.empty_like(ids)
+        _check(lib().wc_moe_sort(ids.data_ptr(), slots, experts, offsets.data_ptr(),
+                                 order.data_ptr(), inverse.data_ptr(), handle), "wc_moe_sort")
+        return MoePlan(offsets, order, inverse)
+    return _run_on(ids.device, stream, run)
+
+
+def _moe_check(t: torch.Tensor, cols: int, what: str, like: torch.Tensor):
+    if t.dtype not in _DTYPES or t.dtype != like.dtype:
+        raise TypeError("%s must be BF16, FP16 or FP32 and of one type; got %s" % (what, t.dtype))
+    return _rows(t, cols, what, like.device)
+
+
+def _moe_inverse(plan: MoePlan, device) -> torch.Tensor:
+    inv = plan.inverse
+    if inv.dim() != 2:
+        raise ValueError("plan.inverse must be (tokens, top)")
+    return _vector(inv, tuple(inv.shape), torch.int32, "plan.inverse", device)
+
+
+def moe_gather(x: torch.Tensor, plan: MoePlan, *, out: torch.Tensor | None = None,
+               stream=None) -> torch.Tensor:
+    """The rows of x (tokens, cols) sorted by expert: (tokens * top, cols), of
+    which plan.offsets[-1] are written (the others are left as they were)."""
+    inv = _moe_inverse(plan, x.device)
+    tokens, top = inv.shape
+    cols = x.shape[-1]
+    _moe_check(x, cols, "x", x)
+    if x.shape[0] != tokens:
+        raise ValueError("x must have %d rows" % tokens)
+    if out is not None:
+        _moe_check(out, cols, "out", x)
+
+    def run(handle):
+        o = torch.empty((tokens * top, cols), dtype=x.dtype, device=x.device) if out is None else out
+        _check(lib().wc_moe_gather(x.data_ptr(), _ld(x), tokens, top, cols, _DTYPES[x.dtype],
+                                   inv.data_ptr(), o.data_ptr(), _ld(o), o.shape[0], handle),
+               "wc_moe_gather")
+        return o
+    return _run_on(x.device, stream, run)
+
+
+def moe_combine(rows: torch.Tensor, plan: MoePlan, weights: torch.Tensor | None, *,
+                out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """out[t] = sum_j weights[t, j] * rows[plan.inverse[t, j]] (weights FP32,
+    None: all 1), in the type of rows."""
+    inv = _moe_inverse(plan, rows.device)
+    tokens, top = inv.shape
+    cols = rows.shape[-1]
+    _moe_check(rows, cols, "rows", rows)
+    if weights is not None:
+        _vector(weights, (tokens, top), torch.float32, "weights", rows.device)
+    if out is not None:
+        _moe_check(out, cols, "out", rows)
+        if out.shape[0] != tokens:
+            raise ValueError("out must have %d rows" % tokens)
+
+    def run(handle):
+        o = torch.empty((tokens, cols), dtype=rows.dtype, device=rows.device) if out is None else out
+        _check(lib().wc_moe_combine(rows.data_ptr(), _ld(rows), rows.shape[0], tokens, top, cols,
+                                    _DTYPES[rows.dtype], inv.data_ptr(),
+                                    None if weights is None else weights.data_ptr(), o.data_ptr(),
+                                    _ld(o), handle), "wc_moe_combine")
+        return o
+    return _run_on(rows.device, stream, run)
+
+
+def moe_gather_backward(drows: torch.Tensor, plan: MoePlan, *, out: torch.Tensor | None = None,
+                        stream=None) -> torch.Tensor:
+    """The gradient of x from that of moe_gather's rows: each token's rows summed."""
+    return moe_combine(drows, plan, None, out=out, stream=stream)
+
+
+def moe_combine_backward(dout: torch.Tensor, rows: torch.Tensor, plan: MoePlan,
+                         weights: torch.Tensor | None, *, drows: torch.Tensor | None = None,
+                         stream=None) -> tuple[torch.Tensor, torch.Tensor]:
+    """The gradients of moe_combine's rows and weights. Rows that no slot names
+    are left as they were in ``drows``."""
+    inv = _moe_inverse(plan, rows.device)
+    tokens, top = inv.shape
+    cols = rows.shape[-1]
+    _moe_check(rows, cols, "rows", rows)
+    _moe_check(dout, cols, "dout", rows)
+    if dout.shape[0] != tokens:
+        raise ValueError("dout must have %d rows" % tokens)
+    if weights is not None:
+        _vector(weights, (tokens, top), torch.float32, "weights", rows.device)
+    if drows is not None:
+        _moe_check(drows, cols, "drows", rows)
+        if drows.shape[0] != rows.shape[0]:
+            raise ValueError("drows must have %d rows" % rows.shape[0])
+
+    def run(handle):
+        d = (torch.empty((rows.shape[0], cols), dtype=rows.dtype, device=rows.device)
+             if drows is None else drows)
+        dw = torch.empty((tokens, top), dtype=torch.float32, device=rows.device)
+        _check(lib().wc_moe_combine_backward(
+            dout.data_ptr(), _ld(dout), rows.data_ptr(), _ld(rows), rows.shape[0], tokens, top,
+            cols, _DTYPES[rows.dtype], inv.data_ptr(),
+            None if weights is None else weights.data_ptr(), d.data_ptr(), _ld(d), dw.data_ptr(),
+            handle), "wc_moe_combine_backward")
+        return d, dw
+    return _run_on(rows.device, stream, run)
