@@ -11,6 +11,9 @@ namespace {
 constexpr uint32_t kStreamFlags = WC_Q4_ZEROS | WC_Q4_SCALES_FP16;
 constexpr uint32_t kAllFlags = kStreamFlags | WC_Q4_X_FP16 | WC_Q4_Y_16BIT;
 
+// Rows of x a matrix up to which wc_q4_gemv.cu is taken.
+constexpr uint64_t kFewRows = 16;
+
 bool aligned(const void* p, uint32_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1u)) == 0; }
 
 bool q4_shape_ok(uint64_t rows, uint64_t cols, uint32_t group) {
@@ -100,7 +103,9 @@ static int q4_product(const void* d_streams, uint64_t stride, uint32_t experts, 
     a.flags = flags;
     a.status = d_status;
     const wc::Q4Layout L = wc::q4_layout(uint32_t(rows), uint32_t(cols), group, flags);
-    return result(wc::launch_q4_gemv(a, L, static_cast<cudaStream_t>(stream)));
+    const uint64_t mean = d_offsets == nullptr ? tokens : (tokens + experts - 1) / experts;
+    const auto launch = mean <= kFewRows ? wc::launch_q4_gemv : wc::launch_q4_gemm;
+    return result(launch(a, L, static_cast<cudaStream_t>(stream)));
 }
 
 int wc_q4_gemm(const void* d_stream, uint64_t stream_bytes, uint64_t rows, uint64_t cols,

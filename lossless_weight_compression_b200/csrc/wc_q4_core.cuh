@@ -159,7 +159,9 @@ cudaError_t launch_q4_pack(const uint8_t* codes, const void* scales, const uint8
                            const Q4Layout& L, uint8_t* out, cudaStream_t stream);
 cudaError_t launch_q4_dequantize(const uint8_t* in, const Q4Layout& L, void* out, uint64_t ld,
                                  uint32_t dtype, int32_t* status, cudaStream_t stream);
+// Products with few rows of x a matrix (wc_q4_gemv.cu) and with many (wc_q4_gemm.cu).
 cudaError_t launch_q4_gemv(const Q4GemmArgs& a, const Q4Layout& L, cudaStream_t stream);
+cudaError_t launch_q4_gemm(const Q4GemmArgs& a, const Q4Layout& L, cudaStream_t stream);
 
 struct MoeArgs {
     uint64_t tokens;

@@ -1,0 +1,711 @@
+// wc_q4_gemm.cu -- products of 4-bit weights with many rows of activations, on
+// the sm_100a tensor cores.
+//
+//   y[p][r] = sum_g s[r][g] * sum_{c in g} (q[r][c] - z[r][g]) * x[p][c]
+//
+// One thread block per SM walks units of 128 weight rows (the MMA's M) times a
+// tile of up to NT rows of x (its N), swept over the columns in slices of 128.
+// Roles joined by mbarrier rings, so that none waits for all the others:
+//   - one thread copies each slice's records (128 rows of codes, scales and
+//     zero points: one contiguous piece) into a ring in shared memory; another
+//     loads the slice's activations by TMA in the 128-byte swizzled K-major
+//     layout the MMA reads B in (two warps with narrower copies when the rows
+//     of x are not 16-byte aligned);
+//   - eight unpacking warps, four per slice in turns, one lane per row, turn
+//     codes into 16-bit integers q - z and store them as the A operand into
+//     tensor memory;
+//   - one thread issues tcgen05.mma, each GROUP of columns into an accumulator
+//     of its own (a ring in tensor memory): the products are exact and a group
+//     sums at most 128 of them;
+//   - eight scaling warps read a group's accumulator (tcgen05.ld), scale it in
+//     FP32 and add it to the row's sums in registers.
+// Scaling sums instead of weights keeps every weight exact (s (q - z) has up to
+// 15 significant bits, a BF16 operand 8) and bounds the unspecified rounding of
+// the tensor cores' accumulation to one group. Its cost is one FP32 FMA per
+// result and group, beside the 1.4 instructions a weight of the unpacking.
+// With few units, the blocks of a cluster share a unit's slices and add their
+// sums through distributed shared memory in a fixed order: y is the same on
+// every run. Every wait is bounded by the device timer.
+#include <cooperative_groups.h>
+#include <string.h>
+
+#include "wc_q4_core.cuh"
+#include "wc_tcgen05.cuh"
+
+namespace wc {
+namespace {
+
+namespace cg = cooperative_groups;
+
+constexpr uint32_t kRowsTile = 128;
+constexpr uint32_t kWRing = 8;        // stages of records
+constexpr uint32_t kMaxXRing4 = 8;    // stages of activations (see x_ring)
+constexpr uint32_t kARing4 = 4;       // A operand stages in tensor memory
+constexpr uint32_t kACol = 256;       // their first column (accumulators below)
+constexpr uint32_t kAccCols = 256;
+constexpr uint32_t kMaxRecBytes = kQ4Codes + 32u * 4u + 64u;
+constexpr uint32_t kWStage = 8 * kMaxRecBytes;
+constexpr uint32_t kSmemMax = 232448;
+
+constexpr int kWWarp = 0, kMWarp = 1, kXWarp0 = 2;  // 2, 3: activations
+constexpr int kXThreads = 64;
+constexpr int kUnpWarp0 = 4;   // 4..11: lane quarter warp % 4, slices of its parity
+constexpr int kSclWarp0 = 12;  // 12..19: lane quarter warp % 4, half of the columns
+constexpr int kSclWarps = 8;
+constexpr int kQ4GemmThreads = 32 * 20;
+
+template <int NT>
+__host__ __device__ constexpr uint32_t x_ring() {
+    return NT == 128 ? 4u : NT == 64 ? 6u : 8u;
+}
+template <int NT>
+__host__ __device__ constexpr uint32_t acc_ring() {
+    return kAccCols / NT > 4 ? 4u : kAccCols / NT;
+}
+
+struct GmParams {
+    CUtensorMap x_map;
+    Q4GemmArgs a;
+    Q4Layout L;
+    uint32_t row_blocks;  // 128-row blocks of a matrix
+    uint32_t tiles;       // one matrix: token tiles, and tokens of a tile
+    uint32_t per_tile;
+    uint32_t split;       // thread blocks that share a unit
+    uint32_t x_bytes;     // alignment of the rows of x: 16 (TMA), 8, 4 or 2
+};
+
+struct GmCtl {
+    unsigned long long w_full[kWRing], w_empty[kWRing];
+    unsigned long long x_full[kMaxXRing4], x_empty[kMaxXRing4];
+    unsigned long long a_full[kARing4], a_empty[kARing4];
+    unsigned long long acc_full[4], acc_empty[4];
+    unsigned long long drain;
+    uint32_t tmem_base;
+    int abort;
+};
+
+struct GmSmem {
+    GmCtl* ctl;
+    uint8_t* x;
+    uint8_t* w;
+    uint32_t* first;   // per expert: first unit (experts + 1 values),
+    uint32_t* lo;      // first row of x,
+    uint32_t* cnt;     // rows
+};
+
+struct GmUnit {
+    uint32_t e, tok0, ntok, rb;
+    bool valid;
+};
+
+// Tiles of cnt rows: as few as NT allows, of equal sizes rounded up to 16.
+template <int NT>
+__device__ __forceinline__ uint32_t tile_rows(uint32_t cnt) {
+    const uint32_t tiles = (cnt + NT - 1) / NT;
+    return ((cnt + tiles - 1) / tiles + 15u) & ~15u;
+}
+
+// Unit u: tiles of one row block are neighbours, so that blocks running at the
+// same time share its records through L2. `e` is where the search starts.
+template <int NT>
+__device__ __forceinline__ GmUnit unit_at(const GmParams& P, const GmSmem& S, uint32_t u,
+                                          uint32_t e) {
+    GmUnit t = {};
+    if (P.a.offsets == nullptr) {
+        t.valid = u < P.row_blocks * P.tiles;
+        t.rb = u / P.tiles;
+        t.tok0 = (u % P.tiles) * P.per_tile;
+        t.ntok = min(P.per_tile, P.a.tokens - t.tok0);
+        return t;
+    }
+    t.valid = u < S.first[P.a.experts];
+    if (!t.valid) return t;
+    while (u >= S.first[e + 1]) ++e;
+    const uint32_t cnt = S.cnt[e], per = tile_rows<NT>(cnt), tiles = (cnt + per - 1) / per;
+    const uint32_t k = u - S.first[e];
+    t.e = e;
+    t.rb = k / tiles;
+    const uint32_t off = (k % tiles) * per;
+    t.tok0 = S.lo[e] + off;
+    t.ntok = min(per, cnt - off);
+    return t;
+}
+
+__device__ __forceinline__ bool gm_wait(unsigned long long* bar, uint32_t parity, GmCtl& c,
+                                        int32_t* status, uint32_t sleep = 0) {
+    if (mbar_wait(bar, parity, &c.abort, sleep)) return true;
+    if (!c.abort) report(status, kStatusTimeout);
+    c.abort = 1;
+    return false;
+}
+
+__device__ __forceinline__ bool gm_wait_warp(unsigned long long* bar, uint32_t parity, GmCtl& c,
+                                             int32_t* status, uint32_t sleep = 0) {
+    return __all_sync(0xFFFFFFFFu, gm_wait(bar, parity, c, status, sleep));
+}
+
+// A ring position: stage and how often the ring went round.
+template <uint32_t N>
+struct Ring {
+    uint32_t s = 0, round = 0;
+    __device__ __forceinline__ void next() {
+        if (++s == N) s = 0, ++round;
+    }
+    __device__ __forceinline__ uint32_t full() const { return round & 1u; }
+    __device__ __forceinline__ uint32_t empty() const { return (round - 1u) & 1u; }
+};
+
+// The slices of a unit that this block takes.
+__device__ __forceinline__ void my_slices(const GmParams& P, uint32_t& s0, uint32_t& s1) {
+    const uint32_t r = blockIdx.x % P.split;
+    s0 = uint32_t(uint64_t(P.L.slices) * r / P.split);
+    s1 = uint32_t(uint64_t(P.L.slices) * (r + 1) / P.split);
+}
+
+template <int NT>
+__device__ void gm_load_w(const GmParams& P, const GmSmem& S) {
+    GmCtl& c = *S.ctl;
+    const Q4Layout& L = P.L;
+    uint32_t s0, s1, e = 0;
+    my_slices(P, s0, s1);
+    Ring<kWRing> w;
+    bool ok = true;
+    for (uint32_t u = blockIdx.x / P.split; ok; u += gridDim.x / P.split) {
+        const GmUnit t = unit_at<NT>(P, S, u, e);
+        if (!t.valid) break;
+        e = t.e;
+        const uint8_t* stream = P.a.stream + t.e * P.a.stride;
+        const uint32_t h = min(8u, L.blocks16 - 8 * t.rb);
+        if (t.rb == 0 && s0 == 0) q4_check_header(stream, L, P.a.status);
+        for (uint32_t s = s0; s < s1; ++s, w.next()) {
+            if (w.round > 0 && !gm_wait(&c.w_empty[w.s], w.empty(), c, P.a.status, 128)) {
+                ok = false;
+                break;
+            }
+            mbar_arrive_expect_tx(&c.w_full[w.s], h * L.rec);
+            bulk_load(S.w + w.s * kWStage, stream + q4_record(L, 8 * t.rb, s), h * L.rec,
+                      &c.w_full[w.s]);
+        }
+    }
+    if (!ok) {  // let the copies already started land before the block ends
+        for (uint32_t k = 0; k < kWRing; ++k) {
+            const uint32_t r = k < w.s ? w.round : w.round - 1u;
+            if (k < w.s || w.round > 0) mbar_wait(&c.w_full[k], r & 1u, nullptr);
+        }
+    }
+}
+
+template <int NT>
+__device__ void gm_load_x_tma(const GmParams& P, const GmSmem& S) {
+    GmCtl& c = *S.ctl;
+    uint32_t s0, s1, e = 0;
+    my_slices(P, s0, s1);
+    constexpr uint32_t XR = x_ring<NT>();
+    Ring<XR> x;
+    bool ok = true;
+    for (uint32_t u = blockIdx.x / P.split; ok; u += gridDim.x / P.split) {
+        const GmUnit t = unit_at<NT>(P, S, u, e);
+        if (!t.valid) break;
+        e = t.e;
+        for (uint32_t s = s0; s < s1; ++s, x.next()) {
+            if (x.round > 0 && !gm_wait(&c.x_empty[x.s], x.empty(), c, P.a.status, 128)) {
+                ok = false;
+                break;
+            }
+            uint8_t* d = S.x + x.s * NT * 256;
+            mbar_arrive_expect_tx(&c.x_full[x.s], NT * 256);
+            tma_load_2d(d, &P.x_map, int32_t(s * kQ4Cols), int32_t(t.tok0), &c.x_full[x.s]);
+            tma_load_2d(d + NT * 128, &P.x_map, int32_t(s * kQ4Cols + 64), int32_t(t.tok0),
+                        &c.x_full[x.s]);
+        }
+    }
+    if (!ok) {
+        for (uint32_t k = 0; k < XR; ++k) {
+            const uint32_t r = k < x.s ? x.round : x.round - 1u;
+            if (k < x.s || x.round > 0) mbar_wait(&c.x_full[k], r & 1u, nullptr);
+        }
+    }
+}
+
+// Rows of x that TMA cannot take: V-byte copies (V = 8, 4: cp.async; 2: through
+// registers) into the same swizzled layout, zeros past the last column. A slice
+// is handed over one slice later, when its copies have landed.
+template <int NT, int V>
+__device__ void gm_load_x_any(const GmParams& P, const GmSmem& S, uint32_t tid) {
+    GmCtl& c = *S.ctl;
+    uint32_t s0, s1, e = 0;
+    my_slices(P, s0, s1);
+    constexpr uint32_t XR = x_ring<NT>();
+    Ring<XR> x;
+    int prev = -1;  // stage not yet handed over
+    auto hand_over = [&](int stage) {
+        fence_proxy_async_smem();
+        mbar_arrive(&c.x_full[stage]);
+    };
+    bool ok = true;
+    for (uint32_t u = blockIdx.x / P.split; ok; u += gridDim.x / P.split) {
+        const GmUnit t = unit_at<NT>(P, S, u, e);
+        if (!t.valid) break;
+        e = t.e;
+        for (uint32_t s = s0; s < s1; ++s, x.next()) {
+            if (x.round > 0 && !gm_wait_warp(&c.x_empty[x.s], x.empty(), c, P.a.status, 128)) {
+                ok = false;
+                break;
+            }
+            const uint32_t base = smem_addr(S.x + x.s * NT * 256);
+            constexpr uint32_t W = V == 2 ? 4 : V;    // bytes a step writes
+            constexpr uint32_t per_row = 256 / W;
+            for (uint32_t k = tid; k < t.ntok * per_row; k += kXThreads) {
+                const uint32_t n = k / per_row, b = (k % per_row) * W;  // row, byte in the slice
+                const uint32_t col = s * kQ4Cols + b / 2;
+                const uint32_t bp = b & 127u;
+                const uint32_t dst = base + (b >> 7) * (NT * 128) + n * 128 +
+                                     ((((bp >> 4) ^ (n & 7u)) << 4) | (bp & 15u));
+                const uint16_t* src =
+                    static_cast<const uint16_t*>(P.a.x) + uint64_t(t.tok0 + n) * P.a.ldx + col;
+                const uint32_t have = col < P.L.cols ? min(W, (P.L.cols - col) * 2) : 0u;
+                if (V == 2) {
+                    const uint32_t v = (have >= 2 ? uint32_t(src[0]) : 0u) |
+                                       (have >= 4 ? uint32_t(src[1]) << 16 : 0u);
+                    asm volatile("st.shared.u32 [%0], %1;" ::"r"(dst), "r"(v) : "memory");
+                } else {
+                    const void* from = have ? static_cast<const void*>(src) : P.a.x;
+                    asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(dst),
+                                 "l"(from), "n"(V), "r"(have)
+                                 : "memory");
+                }
+            }
+            asm volatile("cp.async.commit_group;" ::: "memory");
+            if (prev >= 0) {
+                asm volatile("cp.async.wait_group 1;" ::: "memory");
+                hand_over(prev);
+            }
+            prev = int(x.s);
+        }
+        if (ok && prev >= 0) {
+            asm volatile("cp.async.wait_group 0;" ::: "memory");
+            hand_over(prev);
+            prev = -1;
+        }
+    }
+    asm volatile("cp.async.wait_group 0;" ::: "memory");
+}
+
+// Unpacking warps 4..11: warps of parity k take the block's slices k, k + 2, ...
+template <int NT, bool HALF, int PER>
+__device__ void gm_unpack(const GmParams& P, const GmSmem& S, int wi, int lane) {
+    GmCtl& c = *S.ctl;
+    const Q4Layout& L = P.L;
+    const uint32_t q = uint32_t(wi) & 3u, turn = uint32_t(wi) >> 2;
+    const uint32_t r = 32u * q + uint32_t(lane);
+    const uint32_t row_at = (r >> 4) * L.rec + (r & 15u) * 16u;
+    const uint32_t zero_at = (r >> 4) * L.rec + kQ4Codes + 32u * PER + (r & 15u);
+    const uint32_t t_lane = c.tmem_base + ((32u * q) << 16) + kACol;
+    uint32_t s0, s1, e = 0, count = 0;
+    my_slices(P, s0, s1);
+    Ring<kWRing> w;
+    Ring<kARing4> a;
+    for (uint32_t u = blockIdx.x / P.split;; u += gridDim.x / P.split) {
+        const GmUnit t = unit_at<NT>(P, S, u, e);
+        if (!t.valid) return;
+        e = t.e;
+        for (uint32_t s = s0; s < s1; ++s, ++count, w.next(), a.next()) {
+            if ((count & 1u) != turn) continue;
+            if (!gm_wait_warp(&c.w_full[w.s], w.full(), c, P.a.status)) return;
+            const uint32_t stage = smem_addr(S.w) + w.s * kWStage;
+            uint4 v[4];
+            uint32_t zp[PER];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) v[k] = lds128(stage + row_at + 256u * k);
+#pragma unroll
+            for (int k = 0; k < PER; ++k) {
+                uint32_t z = 8;
+                if (L.zeros)
+                    asm volatile("ld.shared.u8 %0, [%1];" : "=r"(z) : "r"(stage + zero_at + 16u * k));
+                zp[k] = q4_zero_pair<HALF>(z);
+            }
+            if (a.round > 0 && !gm_wait_warp(&c.a_empty[a.s], a.empty(), c, P.a.status)) return;
+            tc_fence_after();
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                uint32_t o[16];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const uint32_t word = i == 0 ? v[k].x : i == 1 ? v[k].y : i == 2 ? v[k].z : v[k].w;
+#pragma unroll
+                    for (int p = 0; p < 4; ++p) o[4 * k + p] = q4_pair<HALF>(word, p, zp[i * PER / 4]);
+                }
+                tmem_st16(t_lane + a.s * 64u + 16u * i, o);
+            }
+            tmem_wait_st();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) {
+                mbar_arrive(&c.w_empty[w.s]);
+                mbar_arrive(&c.a_full[a.s]);
+            }
+        }
+    }
+}
+
+template <int NT, bool HALF, int PER>
+__device__ void gm_mma(const GmParams& P, const GmSmem& S) {
+    GmCtl& c = *S.ctl;
+    const uint32_t x0 = smem_addr(S.x);
+    uint32_t s0, s1, e = 0;
+    my_slices(P, s0, s1);
+    Ring<kARing4> a;
+    Ring<x_ring<NT>()> x;
+    Ring<acc_ring<NT>()> d;
+    bool ok = true, issued = false;
+    for (uint32_t u = blockIdx.x / P.split; ok; u += gridDim.x / P.split) {
+        const GmUnit t = unit_at<NT>(P, S, u, e);
+        if (!t.valid) break;
+        e = t.e;
+        // kind::f16: FP32 accumulator, A and B both BF16 or both FP16 (0 in bits 7-12)
+        const uint32_t n = (t.ntok + 15u) & ~15u;
+        const uint32_t idesc = HALF ? bf16_idesc(kRowsTile, n) & ~((1u << 7) | (1u << 10))
+                                    : bf16_idesc(kRowsTile, n);
+        for (uint32_t s = s0; ok && s < s1; ++s, a.next(), x.next()) {
+            if (!gm_wait(&c.a_full[a.s], a.full(), c, P.a.status) ||
+                !gm_wait(&c.x_full[x.s], x.full(), c, P.a.status)) {
+                ok = false;
+                break;
+            }
+            tc_fence_after();
+            const uint32_t ta = c.tmem_base + kACol + a.s * 64u;
+            const uint64_t xd0 = sw128_desc(x0 + x.s * (NT * 256));
+            const uint64_t xd1 = xd0 + NT * 8;
+#pragma unroll
+            for (int g = 0; g < PER; ++g, d.next()) {
+                if (d.round > 0 && !gm_wait(&c.acc_empty[d.s], d.empty(), c, P.a.status)) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+                const uint32_t acc = c.tmem_base + d.s * NT;
+#pragma unroll
+                for (int k = 0; k < 8 / PER; ++k) {
+                    const int kk = g * (8 / PER) + k;
+                    umma_bf16_ts(acc, ta + 8u * kk, (kk < 4 ? xd0 : xd1) + 2u * (kk & 3), idesc,
+                                 k > 0 ? 1u : 0u);
+                }
+                issued = true;
+                umma_commit(&c.acc_full[d.s]);
+            }
+            umma_commit(&c.a_empty[a.s]);
+            umma_commit(&c.x_empty[x.s]);
+        }
+    }
+    if (issued) {  // every MMA has finished before the block ends
+        umma_commit(&c.drain);
+        mbar_wait(&c.drain, 0, nullptr);
+    }
+}
+
+template <bool HALF>
+__device__ __forceinline__ void store_y(const GmParams& P, uint64_t tok, uint32_t row, float v) {
+    if (P.a.flags & kQ4Y16)
+        static_cast<uint16_t*>(P.a.y)[tok * P.a.ldy + row] =
+            HALF ? __half_as_ushort(__float2half_rn(v)) : __bfloat16_as_ushort(__float2bfloat16_rn(v));
+    else
+        static_cast<float*>(P.a.y)[tok * P.a.ldy + row] = v;
+}
+
+template <int NT, bool HALF, int PER>
+__device__ void gm_scale(const GmParams& P, const GmSmem& S, int wi, int lane) {
+    GmCtl& c = *S.ctl;
+    const Q4Layout& L = P.L;
+    constexpr int HN = NT / 2;  // columns of this warp
+    const uint32_t q = uint32_t(wi) & 3u, half = uint32_t(wi) >> 2;
+    const uint32_t r = 32u * q + uint32_t(lane);
+    const uint32_t scale_at = (r >> 4) * L.rec + kQ4Codes + (r & 15u) * 2u;
+    const uint32_t t_lane = c.tmem_base + ((32u * q) << 16) + half * HN;
+    uint32_t s0, s1, e = 0;
+    my_slices(P, s0, s1);
+    Ring<kWRing> w;
+    Ring<acc_ring<NT>()> d;
+    for (uint32_t u = blockIdx.x / P.split;; u += gridDim.x / P.split) {
+        const GmUnit t = unit_at<NT>(P, S, u, e);
+        if (!t.valid) return;
+        e = t.e;
+        float sum[HN];
+#pragma unroll
+        for (int k = 0; k < HN; ++k) sum[k] = 0.f;
+        const uint32_t live = t.ntok > half * HN ? t.ntok - half * HN : 0u;  // columns in use
+        for (uint32_t s = s0; s < s1; ++s, w.next()) {
+            if (!gm_wait_warp(&c.w_full[w.s], w.full(), c, P.a.status, 64)) return;
+            float sc[PER];
+#pragma unroll
+            for (int g = 0; g < PER; ++g) {
+                uint16_t b;
+                asm volatile("ld.shared.u16 %0, [%1];"
+                             : "=h"(b)
+                             : "r"(smem_addr(S.w) + w.s * kWStage + scale_at + 32u * g));
+                sc[g] = q4_scale(b, L.half_scales);
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&c.w_empty[w.s]);
+#pragma unroll
+            for (int g = 0; g < PER; ++g, d.next()) {
+                if (!gm_wait_warp(&c.acc_full[d.s], d.full(), c, P.a.status, 64)) return;
+                tc_fence_after();
+#pragma unroll
+                for (int k = 0; k < HN; k += 16) {
+                    if (uint32_t(k) < live) {
+                        uint32_t v[16];
+                        tmem_ld16(t_lane + d.s * NT + k, v);
+#pragma unroll
+                        for (int i = 0; i < 16; ++i)
+                            sum[k + i] = fmaf(sc[g], __uint_as_float(v[i]), sum[k + i]);
+                    }
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&c.acc_empty[d.s]);
+            }
+        }
+        if (P.split == 1) {
+            const uint32_t row = t.rb * kRowsTile + r;
+            if (row < L.rows) {
+#pragma unroll
+                for (int k = 0; k < HN; ++k)
+                    if (uint32_t(k) < live)
+                        store_y<HALF>(P, uint64_t(t.tok0) + half * HN + k, row, sum[k]);
+            }
+        } else {  // the block's only unit: every copy into the ring has been used
+            float* red = reinterpret_cast<float*>(S.x);
+#pragma unroll
+            for (int k = 0; k < HN; ++k) red[(half * HN + k) * kRowsTile + r] = sum[k];
+        }
+    }
+}
+
+template <int NT, bool HALF, int PER>
+__global__ void __launch_bounds__(kQ4GemmThreads, 1)
+    q4_gemm_kernel(const __grid_constant__ GmParams P) {
+    extern __shared__ __align__(1024) unsigned char smem_raw[];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    uint8_t* p = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
+    GmSmem S;
+    S.x = p;
+    p += x_ring<NT>() * NT * 256;
+    S.w = p;
+    p += kWRing * kWStage;
+    S.ctl = reinterpret_cast<GmCtl*>(p);
+    p += (sizeof(GmCtl) + 15) / 16 * 16;
+    S.first = reinterpret_cast<uint32_t*>(p);
+    S.lo = S.first + P.a.experts + 1;
+    S.cnt = S.lo + P.a.experts;
+    GmCtl& c = *S.ctl;
+    if (tid == 0) {
+        for (uint32_t s = 0; s < kWRing; ++s) {
+            mbar_init(&c.w_full[s], 1);
+            mbar_init(&c.w_empty[s], 4 + kSclWarps);
+        }
+        for (uint32_t s = 0; s < kMaxXRing4; ++s) {
+            mbar_init(&c.x_full[s], P.x_bytes == 16 ? 1 : kXThreads);
+            mbar_init(&c.x_empty[s], 1);
+        }
+        for (uint32_t s = 0; s < kARing4; ++s) {
+            mbar_init(&c.a_full[s], 4);
+            mbar_init(&c.a_empty[s], 1);
+        }
+        for (uint32_t s = 0; s < 4; ++s) {
+            mbar_init(&c.acc_full[s], 1);
+            mbar_init(&c.acc_empty[s], kSclWarps);
+        }
+        mbar_init(&c.drain, 1);
+        c.abort = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    if (warp == kMWarp) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                         smem_addr(&c.tmem_base)),
+                     "r"(512)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
+    if (P.a.offsets != nullptr) {  // the experts' rows and first units
+        const int total = int(P.a.tokens);
+        for (uint32_t e = tid; e < P.a.experts; e += kQ4GemmThreads) {
+            const int lo = min(max(P.a.offsets[e], 0), total);
+            const int hi = min(max(P.a.offsets[e + 1], lo), total);
+            const uint32_t cnt = uint32_t(hi - lo);
+            S.lo[e] = uint32_t(lo);
+            S.cnt[e] = cnt;
+            const uint32_t per = cnt ? tile_rows<NT>(cnt) : 1u;
+            S.first[e + 1] = (cnt + per - 1) / per * P.row_blocks;
+        }
+        __syncthreads();
+        if (warp == 0) {
+            uint32_t run = 0;
+            for (uint32_t e0 = 0; e0 < P.a.experts; e0 += 32) {
+                const uint32_t e = e0 + lane;
+                uint32_t v = e < P.a.experts ? S.first[e + 1] : 0u;
+#pragma unroll
+                for (int o = 1; o < 32; o *= 2) {
+                    const uint32_t x = __shfl_up_sync(0xFFFFFFFFu, v, o);
+                    if (lane >= o) v += x;
+                }
+                if (e < P.a.experts) S.first[e + 1] = run + v;
+                run += __shfl_sync(0xFFFFFFFFu, v, 31);
+            }
+            if (lane == 0) S.first[0] = 0;
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+
+    if (warp == kWWarp) {
+        if (lane == 0) gm_load_w<NT>(P, S);
+    } else if (warp == kMWarp) {
+        if (lane == 0) gm_mma<NT, HALF, PER>(P, S);
+    } else if (warp < kUnpWarp0) {
+        if (P.x_bytes == 16) {
+            if (tid == 32 * kXWarp0) gm_load_x_tma<NT>(P, S);
+        } else if (P.x_bytes == 8) {
+            gm_load_x_any<NT, 8>(P, S, tid - 32 * kXWarp0);
+        } else if (P.x_bytes == 4) {
+            gm_load_x_any<NT, 4>(P, S, tid - 32 * kXWarp0);
+        } else {
+            gm_load_x_any<NT, 2>(P, S, tid - 32 * kXWarp0);
+        }
+    } else if (warp < kSclWarp0) {
+        gm_unpack<NT, HALF, PER>(P, S, warp - kUnpWarp0, lane);
+    } else {
+        gm_scale<NT, HALF, PER>(P, S, warp - kSclWarp0, lane);
+    }
+    __syncwarp();
+    if (P.split > 1) {
+        // each block of the cluster adds and writes its share of the tokens
+        cg::cluster_group cluster = cg::this_cluster();
+        cluster.sync();
+        const GmUnit t = unit_at<NT>(P, S, blockIdx.x / P.split, 0);
+        if (t.valid) {
+            const uint32_t rank = blockIdx.x % P.split;
+            const float* red = reinterpret_cast<const float*>(S.x);
+            const uint32_t t0 = t.ntok * rank / P.split, t1 = t.ntok * (rank + 1) / P.split;
+            for (uint32_t k = t0 * kRowsTile + tid; k < t1 * kRowsTile; k += kQ4GemmThreads) {
+                float v = 0.f;
+                for (uint32_t b = 0; b < P.split; ++b) v += cluster.map_shared_rank(red, b)[k];
+                const uint32_t row = t.rb * kRowsTile + k % kRowsTile;
+                if (row < P.L.rows) store_y<HALF>(P, uint64_t(t.tok0) + k / kRowsTile, row, v);
+            }
+        }
+        cluster.sync();
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == kMWarp) {
+        tc_fence_after();
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(c.tmem_base),
+                     "r"(512)
+                     : "memory");
+    }
+}
+
+template <int NT>
+uint32_t gm_smem(uint32_t experts) {
+    return 1024 + x_ring<NT>() * NT * 256 + kWRing * kWStage + (sizeof(GmCtl) + 15) / 16 * 16 +
+           (3 * experts + 1) * 4;
+}
+
+template <int NT, bool HALF, int PER>
+cudaError_t gm_launch(GmParams& P, uint32_t sms, uint32_t units, cudaStream_t stream) {
+    static std::mutex mu;
+    static bool set[64];
+    int dev = 0;
+    cudaError_t err = cudaGetDevice(&dev);
+    if (err != cudaSuccess) return err;
+    if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+    const auto kernel = q4_gemm_kernel<NT, HALF, PER>;
+    {
+        std::lock_guard<std::mutex> lock(mu);
+        if (!set[dev]) {
+            err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       int(kSmemMax));
+            if (err != cudaSuccess) return err;
+            set[dev] = true;
+        }
+    }
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(P.split > 1 ? units * P.split : units < sms ? units : sms);
+    cfg.blockDim = dim3(kQ4GemmThreads);
+    cfg.dynamicSmemBytes = gm_smem<NT>(P.a.experts);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = P.split;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = P.split > 1 ? 1 : 0;
+    return cudaLaunchKernelEx(&cfg, kernel, P);
+}
+
+template <int NT>
+cudaError_t gm_tokens(GmParams& P, cudaStream_t stream) {
+    int dev = 0, sms = 0;
+    cudaError_t err = cudaGetDevice(&dev);
+    if (err == cudaSuccess) err = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    if (err != cudaSuccess) return err;
+    P.row_blocks = (P.L.blocks16 + 7) / 8;
+    const uint32_t T = P.a.tokens;
+    uint64_t units;
+    if (P.a.offsets == nullptr) {
+        const uint32_t tiles = (T + NT - 1) / NT;
+        P.per_tile = ((T + tiles - 1) / tiles + 15u) & ~15u;
+        P.tiles = (T + P.per_tile - 1) / P.per_tile;
+        units = uint64_t(P.row_blocks) * P.tiles;
+    } else {  // at most: every expert with rows ends in a partial tile
+        units = uint64_t(P.row_blocks) * (T / NT + (T < P.a.experts ? T : P.a.experts));
+    }
+    if (units > 0x7FFFFFFFull) return cudaErrorInvalidValue;
+    P.split = 1;
+    if (P.a.offsets == nullptr)
+        while (P.split < 8 && units * P.split * 2 <= uint64_t(sms) && P.L.slices / (2 * P.split) >= 4)
+            P.split *= 2;
+    if (P.x_bytes == 16) {
+        PFN_cuTensorMapEncodeTiled_v12000 enc = encode_fn();
+        if (enc == nullptr) return cudaErrorNotSupported;
+        const bool half = P.a.flags & kQ4XHalf;
+        const cuuint64_t dims[2] = {P.L.cols, T};
+        const cuuint64_t strides[1] = {P.a.ldx * 2};
+        const cuuint32_t box[2] = {64, NT};
+        const cuuint32_t estr[2] = {1, 1};
+        if (enc(&P.x_map, half ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2,
+                const_cast<void*>(P.a.x), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+            return cudaErrorInvalidValue;
+    }
+    const uint32_t u = uint32_t(units), n = uint32_t(sms);
+    if (P.a.flags & kQ4XHalf)
+        return P.L.per == 1   ? gm_launch<NT, true, 1>(P, n, u, stream)
+               : P.L.per == 2 ? gm_launch<NT, true, 2>(P, n, u, stream)
+                              : gm_launch<NT, true, 4>(P, n, u, stream);
+    return P.L.per == 1   ? gm_launch<NT, false, 1>(P, n, u, stream)
+           : P.L.per == 2 ? gm_launch<NT, false, 2>(P, n, u, stream)
+                          : gm_launch<NT, false, 4>(P, n, u, stream);
+}
+
+}  // namespace
+
+cudaError_t launch_q4_gemm(const Q4GemmArgs& a, const Q4Layout& L, cudaStream_t stream) {
+    if (L.rows == 0 || a.tokens == 0) return cudaSuccess;
+    GmParams P;
+    memset(&P, 0, sizeof(P));
+    P.a = a;
+    P.L = L;
+    // a tensor map wants 16-byte rows and at most 2^40 bytes between them
+    const uint64_t al = reinterpret_cast<uintptr_t>(a.x) | (a.ldx * 2);
+    P.x_bytes = al % 16 == 0 && a.ldx < (1ull << 38) ? 16u : al % 8 == 0 ? 8u : al % 4 == 0 ? 4u : 2u;
+    // rows of x that a matrix takes: the tile's size follows
+    const uint32_t rows = a.offsets == nullptr ? a.tokens : (a.tokens + a.experts - 1) / a.experts;
+    if (rows > 64) return gm_tokens<128>(P, stream);
+    if (rows > 32) return gm_tokens<64>(P, stream);
+    return gm_tokens<32>(P, stream);
+}
+
+}  // namespace wc
