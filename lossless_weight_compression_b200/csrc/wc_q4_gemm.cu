@@ -14,9 +14,9 @@
 //   - eight unpacking warps, four per slice in turns, one lane per row, turn
 //     codes into 16-bit integers q - z and store them as the A operand into
 //     tensor memory;
-//   - one thread issues tcgen05.mma, each GROUP of columns into an accumulator
-//     of its own (a ring in tensor memory): the products are exact and a group
-//     sums at most 128 of them;
+//   - two threads issue tcgen05.mma for slices in turns, each GROUP of columns
+//     into an accumulator of its own in tensor memory: the products are exact
+//     and a group sums at most 128 of them;
 //   - eight scaling warps read a group's accumulator (tcgen05.ld), scale it in
 //     FP32 and add it to the row's sums in registers.
 // Scaling sums instead of weights keeps every weight exact (s (q - z) has up to
@@ -39,29 +39,37 @@ namespace cg = cooperative_groups;
 
 constexpr uint32_t kRowsTile = 128;
 constexpr uint32_t kWRing = 8;        // stages of records
-constexpr uint32_t kMaxXRing4 = 8;    // stages of activations (see x_ring)
-constexpr uint32_t kARing4 = 4;       // A operand stages in tensor memory
+constexpr uint32_t kSRing = 4;        // stages of a slice's operands: x in shared memory, A in
+                                      // tensor memory
 constexpr uint32_t kACol = 256;       // their first column (accumulators below)
 constexpr uint32_t kAccCols = 256;
 constexpr uint32_t kMaxRecBytes = kQ4Codes + 32u * 4u + 64u;
 constexpr uint32_t kWStage = 8 * kMaxRecBytes;
 constexpr uint32_t kSmemMax = 232448;
 
-constexpr int kWWarp = 0, kMWarp = 1, kXWarp0 = 2;  // 2, 3: activations
-constexpr int kXThreads = 64;
+constexpr int kWWarp = 0, kMWarp0 = 2;  // 1: activations; 2, 3: MMA issue, slices in turns
+constexpr int kMWarps = 2;
 constexpr int kUnpWarp0 = 4;   // 4..11: lane quarter warp % 4, slices of its parity
 constexpr int kSclWarp0 = 12;  // 12..19: lane quarter warp % 4, half of the columns
 constexpr int kSclWarps = 8;
 constexpr int kQ4GemmThreads = 32 * 20;
 
-template <int NT>
-__host__ __device__ constexpr uint32_t x_ring() {
-    return NT == 128 ? 4u : NT == 64 ? 6u : 8u;
-}
-template <int NT>
-__host__ __device__ constexpr uint32_t acc_ring() {
-    return kAccCols / NT > 4 ? 4u : kAccCols / NT;
-}
+// Registers of a thread after the roles split (of 96 at launch: 4 x 48 +
+// 8 x 64 + 8 x 152 warps = 20 x 96): a scaling warp holds up to 64 sums and as
+// many results on their way.
+constexpr int kRegsIssue = 48, kRegsUnpack = 64, kRegsScale = 152;
+static_assert(4 * kRegsIssue + 8 * kRegsUnpack + 8 * kRegsScale == 20 * 96, "register split");
+
+// Accumulators of NT columns. Where they hold two slices' groups or more, the
+// scaling warps' word that a slice's accumulators are free is one more arrival
+// on the barrier that hands its operands over (an issuing thread's every wait
+// delays its next MMA); else the groups go round a ring with barriers of its own.
+template <int NT, int PER>
+struct Acc {
+    static constexpr uint32_t ring = kAccCols / NT;
+    static constexpr bool by_slice = ring >= 2 * PER;
+    static constexpr uint32_t slices = by_slice ? (ring / PER > kSRing ? kSRing : ring / PER) : 1;
+};
 
 struct GmParams {
     CUtensorMap x_map;
@@ -76,10 +84,11 @@ struct GmParams {
 
 struct GmCtl {
     unsigned long long w_full[kWRing], w_empty[kWRing];
-    unsigned long long x_full[kMaxXRing4], x_empty[kMaxXRing4];
-    unsigned long long a_full[kARing4], a_empty[kARing4];
-    unsigned long long acc_full[4], acc_empty[4];
-    unsigned long long drain;
+    unsigned long long s_full[kSRing];     // x and A of a slice (and free accumulators)
+    unsigned long long done[kSRing][4];    // the MMAs of a slice's groups
+    unsigned long long acc_empty[4];       // !by_slice: accumulator ring,
+    unsigned long long order[kMWarps];     //   and the issuing threads' turns at it
+    unsigned long long drain[kMWarps];
     uint32_t tmem_base;
     int abort;
 };
@@ -195,34 +204,33 @@ __device__ void gm_load_w(const GmParams& P, const GmSmem& S) {
     }
 }
 
-template <int NT>
+template <int NT, int PER>
 __device__ void gm_load_x_tma(const GmParams& P, const GmSmem& S) {
     GmCtl& c = *S.ctl;
     uint32_t s0, s1, e = 0;
     my_slices(P, s0, s1);
-    constexpr uint32_t XR = x_ring<NT>();
-    Ring<XR> x;
+    Ring<kSRing> x;
     bool ok = true;
     for (uint32_t u = blockIdx.x / P.split; ok; u += gridDim.x / P.split) {
         const GmUnit t = unit_at<NT>(P, S, u, e);
         if (!t.valid) break;
         e = t.e;
         for (uint32_t s = s0; s < s1; ++s, x.next()) {
-            if (x.round > 0 && !gm_wait(&c.x_empty[x.s], x.empty(), c, P.a.status, 128)) {
+            if (x.round > 0 && !gm_wait(&c.done[x.s][PER - 1], x.empty(), c, P.a.status, 128)) {
                 ok = false;
                 break;
             }
             uint8_t* d = S.x + x.s * NT * 256;
-            mbar_arrive_expect_tx(&c.x_full[x.s], NT * 256);
-            tma_load_2d(d, &P.x_map, int32_t(s * kQ4Cols), int32_t(t.tok0), &c.x_full[x.s]);
+            mbar_arrive_expect_tx(&c.s_full[x.s], NT * 256);
+            tma_load_2d(d, &P.x_map, int32_t(s * kQ4Cols), int32_t(t.tok0), &c.s_full[x.s]);
             tma_load_2d(d + NT * 128, &P.x_map, int32_t(s * kQ4Cols + 64), int32_t(t.tok0),
-                        &c.x_full[x.s]);
+                        &c.s_full[x.s]);
         }
     }
-    if (!ok) {
-        for (uint32_t k = 0; k < XR; ++k) {
+    if (!ok) {  // (bounded: an aborted slice's other arrivals may never come)
+        for (uint32_t k = 0; k < kSRing; ++k) {
             const uint32_t r = k < x.s ? x.round : x.round - 1u;
-            if (k < x.s || x.round > 0) mbar_wait(&c.x_full[k], r & 1u, nullptr);
+            if (k < x.s || x.round > 0) mbar_wait(&c.s_full[k], r & 1u, nullptr);
         }
     }
 }
@@ -230,17 +238,16 @@ __device__ void gm_load_x_tma(const GmParams& P, const GmSmem& S) {
 // Rows of x that TMA cannot take: V-byte copies (V = 8, 4: cp.async; 2: through
 // registers) into the same swizzled layout, zeros past the last column. A slice
 // is handed over one slice later, when its copies have landed.
-template <int NT, int V>
+template <int NT, int PER, int V>
 __device__ void gm_load_x_any(const GmParams& P, const GmSmem& S, uint32_t tid) {
     GmCtl& c = *S.ctl;
     uint32_t s0, s1, e = 0;
     my_slices(P, s0, s1);
-    constexpr uint32_t XR = x_ring<NT>();
-    Ring<XR> x;
+    Ring<kSRing> x;
     int prev = -1;  // stage not yet handed over
     auto hand_over = [&](int stage) {
         fence_proxy_async_smem();
-        mbar_arrive(&c.x_full[stage]);
+        mbar_arrive(&c.s_full[stage]);
     };
     bool ok = true;
     for (uint32_t u = blockIdx.x / P.split; ok; u += gridDim.x / P.split) {
@@ -248,14 +255,14 @@ __device__ void gm_load_x_any(const GmParams& P, const GmSmem& S, uint32_t tid) 
         if (!t.valid) break;
         e = t.e;
         for (uint32_t s = s0; s < s1; ++s, x.next()) {
-            if (x.round > 0 && !gm_wait_warp(&c.x_empty[x.s], x.empty(), c, P.a.status, 128)) {
+            if (x.round > 0 && !gm_wait_warp(&c.done[x.s][PER - 1], x.empty(), c, P.a.status, 128)) {
                 ok = false;
                 break;
             }
             const uint32_t base = smem_addr(S.x + x.s * NT * 256);
             constexpr uint32_t W = V == 2 ? 4 : V;    // bytes a step writes
             constexpr uint32_t per_row = 256 / W;
-            for (uint32_t k = tid; k < t.ntok * per_row; k += kXThreads) {
+            for (uint32_t k = tid; k < t.ntok * per_row; k += 32) {
                 const uint32_t n = k / per_row, b = (k % per_row) * W;  // row, byte in the slice
                 const uint32_t col = s * kQ4Cols + b / 2;
                 const uint32_t bp = b & 127u;
@@ -304,7 +311,7 @@ __device__ void gm_unpack(const GmParams& P, const GmSmem& S, int wi, int lane) 
     uint32_t s0, s1, e = 0, count = 0;
     my_slices(P, s0, s1);
     Ring<kWRing> w;
-    Ring<kARing4> a;
+    Ring<kSRing> a;
     for (uint32_t u = blockIdx.x / P.split;; u += gridDim.x / P.split) {
         const GmUnit t = unit_at<NT>(P, S, u, e);
         if (!t.valid) return;
@@ -324,7 +331,7 @@ __device__ void gm_unpack(const GmParams& P, const GmSmem& S, int wi, int lane) 
                     asm volatile("ld.shared.u8 %0, [%1];" : "=r"(z) : "r"(stage + zero_at + 16u * k));
                 zp[k] = q4_zero_pair<HALF>(z);
             }
-            if (a.round > 0 && !gm_wait_warp(&c.a_empty[a.s], a.empty(), c, P.a.status)) return;
+            if (a.round > 0 && !gm_wait_warp(&c.done[a.s][PER - 1], a.empty(), c, P.a.status)) return;
             tc_fence_after();
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
@@ -342,21 +349,22 @@ __device__ void gm_unpack(const GmParams& P, const GmSmem& S, int wi, int lane) 
             __syncwarp();
             if (lane == 0) {
                 mbar_arrive(&c.w_empty[w.s]);
-                mbar_arrive(&c.a_full[a.s]);
+                mbar_arrive(&c.s_full[a.s]);
             }
         }
     }
 }
 
+// Issue of the block's slices k, k + 2, ... (k = turn): what a thread does
+// between two slices' MMAs (some 300 cycles of waits and commits beside their
+// 400 to 500) overlaps the other's.
 template <int NT, bool HALF, int PER>
-__device__ void gm_mma(const GmParams& P, const GmSmem& S) {
+__device__ void gm_mma(const GmParams& P, const GmSmem& S, uint32_t turn) {
     GmCtl& c = *S.ctl;
+    using A = Acc<NT, PER>;
     const uint32_t x0 = smem_addr(S.x);
-    uint32_t s0, s1, e = 0;
+    uint32_t s0, s1, e = 0, count = 0;
     my_slices(P, s0, s1);
-    Ring<kARing4> a;
-    Ring<x_ring<NT>()> x;
-    Ring<acc_ring<NT>()> d;
     bool ok = true, issued = false;
     for (uint32_t u = blockIdx.x / P.split; ok; u += gridDim.x / P.split) {
         const GmUnit t = unit_at<NT>(P, S, u, e);
@@ -366,24 +374,40 @@ __device__ void gm_mma(const GmParams& P, const GmSmem& S) {
         const uint32_t n = (t.ntok + 15u) & ~15u;
         const uint32_t idesc = HALF ? bf16_idesc(kRowsTile, n) & ~((1u << 7) | (1u << 10))
                                     : bf16_idesc(kRowsTile, n);
-        for (uint32_t s = s0; ok && s < s1; ++s, a.next(), x.next()) {
-            if (!gm_wait(&c.a_full[a.s], a.full(), c, P.a.status) ||
-                !gm_wait(&c.x_full[x.s], x.full(), c, P.a.status)) {
+        for (uint32_t s = s0; ok && s < s1; ++s, ++count) {
+            if (count % kMWarps != turn) continue;
+            const uint32_t st = count % kSRing, round = count / kSRing;
+            const uint32_t ta = c.tmem_base + kACol + st * 64u;
+            const uint64_t xd0 = sw128_desc(x0 + st * (NT * 256));
+            const uint64_t xd1 = xd0 + NT * 8;
+            if (!gm_wait(&c.s_full[st], round & 1u, c, P.a.status)) {
+                ok = false;
+                break;
+            }
+            // The accumulator ring is waited for in order: a thread that came
+            // to it a slice early would take an older phase for its own.
+            if (!A::by_slice && count > 0 &&
+                !gm_wait(&c.order[turn], ((count - 1) / kMWarps) & 1u, c, P.a.status)) {
                 ok = false;
                 break;
             }
             tc_fence_after();
-            const uint32_t ta = c.tmem_base + kACol + a.s * 64u;
-            const uint64_t xd0 = sw128_desc(x0 + x.s * (NT * 256));
-            const uint64_t xd1 = xd0 + NT * 8;
 #pragma unroll
-            for (int g = 0; g < PER; ++g, d.next()) {
-                if (d.round > 0 && !gm_wait(&c.acc_empty[d.s], d.empty(), c, P.a.status)) {
-                    ok = false;
-                    break;
+            for (int g = 0; g < PER; ++g) {
+                uint32_t d;
+                if (A::by_slice) {
+                    d = (count % A::slices) * PER + g;
+                } else {
+                    const uint32_t gi = count * PER + g;
+                    d = gi % A::ring;
+                    if (gi / A::ring > 0 &&
+                        !gm_wait(&c.acc_empty[d], (gi / A::ring - 1u) & 1u, c, P.a.status)) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
                 }
-                tc_fence_after();
-                const uint32_t acc = c.tmem_base + d.s * NT;
+                const uint32_t acc = c.tmem_base + d * NT;
 #pragma unroll
                 for (int k = 0; k < 8 / PER; ++k) {
                     const int kk = g * (8 / PER) + k;
@@ -391,15 +415,14 @@ __device__ void gm_mma(const GmParams& P, const GmSmem& S) {
                                  k > 0 ? 1u : 0u);
                 }
                 issued = true;
-                umma_commit(&c.acc_full[d.s]);
+                if (!A::by_slice && g == PER - 1) mbar_arrive(&c.order[turn ^ 1u]);
+                umma_commit(&c.done[st][g]);
             }
-            umma_commit(&c.a_empty[a.s]);
-            umma_commit(&c.x_empty[x.s]);
         }
     }
     if (issued) {  // every MMA has finished before the block ends
-        umma_commit(&c.drain);
-        mbar_wait(&c.drain, 0, nullptr);
+        umma_commit(&c.drain[turn]);
+        mbar_wait(&c.drain[turn], 0, nullptr);
     }
 }
 
@@ -412,28 +435,78 @@ __device__ __forceinline__ void store_y(const GmParams& P, uint64_t tok, uint32_
         static_cast<float*>(P.a.y)[tok * P.a.ldy + row] = v;
 }
 
+// HN consecutive FP32 columns of this thread's tensor memory lane.
+__device__ __forceinline__ void tmem_ld_cols(uint32_t a, uint32_t (&v)[16]) { tmem_ld16(a, v); }
+__device__ __forceinline__ void tmem_ld_cols(uint32_t a, uint32_t (&v)[32]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,"
+        "%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+        : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]),
+          "=r"(v[7]), "=r"(v[8]), "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]),
+          "=r"(v[14]), "=r"(v[15]), "=r"(v[16]), "=r"(v[17]), "=r"(v[18]), "=r"(v[19]),
+          "=r"(v[20]), "=r"(v[21]), "=r"(v[22]), "=r"(v[23]), "=r"(v[24]), "=r"(v[25]),
+          "=r"(v[26]), "=r"(v[27]), "=r"(v[28]), "=r"(v[29]), "=r"(v[30]), "=r"(v[31])
+        : "r"(a));
+    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void tmem_ld_cols(uint32_t a, uint32_t (&v)[64]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x64.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,"
+        "%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32,%33,%34,%35,%36,"
+        "%37,%38,%39,%40,%41,%42,%43,%44,%45,%46,%47,%48,%49,%50,%51,%52,%53,%54,%55,%56,%57,%58,"
+        "%59,%60,%61,%62,%63}, [%64];"
+        : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]),
+          "=r"(v[7]), "=r"(v[8]), "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]),
+          "=r"(v[14]), "=r"(v[15]), "=r"(v[16]), "=r"(v[17]), "=r"(v[18]), "=r"(v[19]),
+          "=r"(v[20]), "=r"(v[21]), "=r"(v[22]), "=r"(v[23]), "=r"(v[24]), "=r"(v[25]),
+          "=r"(v[26]), "=r"(v[27]), "=r"(v[28]), "=r"(v[29]), "=r"(v[30]), "=r"(v[31]),
+          "=r"(v[32]), "=r"(v[33]), "=r"(v[34]), "=r"(v[35]), "=r"(v[36]), "=r"(v[37]),
+          "=r"(v[38]), "=r"(v[39]), "=r"(v[40]), "=r"(v[41]), "=r"(v[42]), "=r"(v[43]),
+          "=r"(v[44]), "=r"(v[45]), "=r"(v[46]), "=r"(v[47]), "=r"(v[48]), "=r"(v[49]),
+          "=r"(v[50]), "=r"(v[51]), "=r"(v[52]), "=r"(v[53]), "=r"(v[54]), "=r"(v[55]),
+          "=r"(v[56]), "=r"(v[57]), "=r"(v[58]), "=r"(v[59]), "=r"(v[60]), "=r"(v[61]),
+          "=r"(v[62]), "=r"(v[63])
+        : "r"(a));
+    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+}
+
+// Two FP32 FMAs in one instruction, each rounded to nearest.
+__device__ __forceinline__ void fma2(float2& acc, float s, uint32_t v0, uint32_t v1) {
+    asm("{\n\t.reg .b64 a, b, d;\n\t"
+        "mov.b64 a, {%2, %2};\n\t"
+        "mov.b64 b, {%3, %4};\n\t"
+        "mov.b64 d, {%0, %1};\n\t"
+        "fma.rn.f32x2 d, a, b, d;\n\t"
+        "mov.b64 {%0, %1}, d;\n\t}"
+        : "+f"(acc.x), "+f"(acc.y)
+        : "f"(s), "r"(v0), "r"(v1));
+}
+
 template <int NT, bool HALF, int PER>
 __device__ void gm_scale(const GmParams& P, const GmSmem& S, int wi, int lane) {
     GmCtl& c = *S.ctl;
     const Q4Layout& L = P.L;
+    using A = Acc<NT, PER>;
     constexpr int HN = NT / 2;  // columns of this warp
     const uint32_t q = uint32_t(wi) & 3u, half = uint32_t(wi) >> 2;
     const uint32_t r = 32u * q + uint32_t(lane);
     const uint32_t scale_at = (r >> 4) * L.rec + kQ4Codes + (r & 15u) * 2u;
     const uint32_t t_lane = c.tmem_base + ((32u * q) << 16) + half * HN;
-    uint32_t s0, s1, e = 0;
+    uint32_t s0, s1, e = 0, count = 0;
     my_slices(P, s0, s1);
     Ring<kWRing> w;
-    Ring<acc_ring<NT>()> d;
+    if (A::by_slice && lane == 0)  // the first slices' accumulators are free
+        for (uint32_t k = 0; k < A::slices; ++k) mbar_arrive(&c.s_full[k]);
     for (uint32_t u = blockIdx.x / P.split;; u += gridDim.x / P.split) {
         const GmUnit t = unit_at<NT>(P, S, u, e);
         if (!t.valid) return;
         e = t.e;
-        float sum[HN];
+        float2 sum[HN / 2];
 #pragma unroll
-        for (int k = 0; k < HN; ++k) sum[k] = 0.f;
+        for (int k = 0; k < HN / 2; ++k) sum[k] = make_float2(0.f, 0.f);
         const uint32_t live = t.ntok > half * HN ? t.ntok - half * HN : 0u;  // columns in use
-        for (uint32_t s = s0; s < s1; ++s, w.next()) {
+        for (uint32_t s = s0; s < s1; ++s, ++count, w.next()) {
+            const uint32_t st = count % kSRing, round = count / kSRing;
             if (!gm_wait_warp(&c.w_full[w.s], w.full(), c, P.a.status, 64)) return;
             float sc[PER];
 #pragma unroll
@@ -447,22 +520,28 @@ __device__ void gm_scale(const GmParams& P, const GmSmem& S, int wi, int lane) {
             __syncwarp();
             if (lane == 0) mbar_arrive(&c.w_empty[w.s]);
 #pragma unroll
-            for (int g = 0; g < PER; ++g, d.next()) {
-                if (!gm_wait_warp(&c.acc_full[d.s], d.full(), c, P.a.status, 64)) return;
+            for (int g = 0; g < PER; ++g) {
+                const uint32_t gi = count * PER + g;
+                const uint32_t d = A::by_slice ? (count % A::slices) * PER + g : gi % A::ring;
+                if (!gm_wait_warp(&c.done[st][g], round & 1u, c, P.a.status, 64)) return;
                 tc_fence_after();
-#pragma unroll
-                for (int k = 0; k < HN; k += 16) {
-                    if (uint32_t(k) < live) {
-                        uint32_t v[16];
-                        tmem_ld16(t_lane + d.s * NT + k, v);
-#pragma unroll
-                        for (int i = 0; i < 16; ++i)
-                            sum[k + i] = fmaf(sc[g], __uint_as_float(v[i]), sum[k + i]);
+                if (live > 0) {
+                    uint32_t v[HN];
+                    tmem_ld_cols(t_lane + d * NT, v);
+                    if (!A::by_slice || g == PER - 1) {
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0)
+                            mbar_arrive(A::by_slice ? &c.s_full[(count + A::slices) % kSRing]
+                                                    : &c.acc_empty[d]);
                     }
+#pragma unroll
+                    for (int k = 0; k < HN / 2; ++k) fma2(sum[k], sc[g], v[2 * k], v[2 * k + 1]);
+                } else if (!A::by_slice || g == PER - 1) {
+                    if (lane == 0)
+                        mbar_arrive(A::by_slice ? &c.s_full[(count + A::slices) % kSRing]
+                                                : &c.acc_empty[d]);
                 }
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&c.acc_empty[d.s]);
             }
         }
         if (P.split == 1) {
@@ -471,12 +550,14 @@ __device__ void gm_scale(const GmParams& P, const GmSmem& S, int wi, int lane) {
 #pragma unroll
                 for (int k = 0; k < HN; ++k)
                     if (uint32_t(k) < live)
-                        store_y<HALF>(P, uint64_t(t.tok0) + half * HN + k, row, sum[k]);
+                        store_y<HALF>(P, uint64_t(t.tok0) + half * HN + k, row,
+                                      k & 1 ? sum[k / 2].y : sum[k / 2].x);
             }
         } else {  // the block's only unit: every copy into the ring has been used
             float* red = reinterpret_cast<float*>(S.x);
 #pragma unroll
-            for (int k = 0; k < HN; ++k) red[(half * HN + k) * kRowsTile + r] = sum[k];
+            for (int k = 0; k < HN; ++k)
+                red[(half * HN + k) * kRowsTile + r] = k & 1 ? sum[k / 2].y : sum[k / 2].x;
         }
     }
 }
@@ -489,7 +570,7 @@ __global__ void __launch_bounds__(kQ4GemmThreads, 1)
     uint8_t* p = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
     GmSmem S;
     S.x = p;
-    p += x_ring<NT>() * NT * 256;
+    p += kSRing * NT * 256;
     S.w = p;
     p += kWRing * kWStage;
     S.ctl = reinterpret_cast<GmCtl*>(p);
@@ -503,23 +584,20 @@ __global__ void __launch_bounds__(kQ4GemmThreads, 1)
             mbar_init(&c.w_full[s], 1);
             mbar_init(&c.w_empty[s], 4 + kSclWarps);
         }
-        for (uint32_t s = 0; s < kMaxXRing4; ++s) {
-            mbar_init(&c.x_full[s], P.x_bytes == 16 ? 1 : kXThreads);
-            mbar_init(&c.x_empty[s], 1);
+        const uint32_t free_acc = Acc<NT, PER>::by_slice ? kSclWarps : 0;
+        for (uint32_t s = 0; s < kSRing; ++s) {
+            mbar_init(&c.s_full[s], 4 + (P.x_bytes == 16 ? 1 : 32) + free_acc);
+            for (int g = 0; g < PER; ++g) mbar_init(&c.done[s][g], 1);
         }
-        for (uint32_t s = 0; s < kARing4; ++s) {
-            mbar_init(&c.a_full[s], 4);
-            mbar_init(&c.a_empty[s], 1);
+        for (uint32_t s = 0; s < 4; ++s) mbar_init(&c.acc_empty[s], kSclWarps);
+        for (int s = 0; s < kMWarps; ++s) {
+            mbar_init(&c.drain[s], 1);
+            mbar_init(&c.order[s], 1);
         }
-        for (uint32_t s = 0; s < 4; ++s) {
-            mbar_init(&c.acc_full[s], 1);
-            mbar_init(&c.acc_empty[s], kSclWarps);
-        }
-        mbar_init(&c.drain, 1);
         c.abort = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
-    if (warp == kMWarp) {
+    if (warp == kMWarp0) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
                          smem_addr(&c.tmem_base)),
                      "r"(512)
@@ -558,24 +636,33 @@ __global__ void __launch_bounds__(kQ4GemmThreads, 1)
     __syncthreads();
     tc_fence_after();
 
-    if (warp == kWWarp) {
-        if (lane == 0) gm_load_w<NT>(P, S);
-    } else if (warp == kMWarp) {
-        if (lane == 0) gm_mma<NT, HALF, PER>(P, S);
-    } else if (warp < kUnpWarp0) {
-        if (P.x_bytes == 16) {
-            if (tid == 32 * kXWarp0) gm_load_x_tma<NT>(P, S);
+    if (warp < kUnpWarp0) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsIssue));
+        if (warp == kWWarp) {
+            if (lane == 0) gm_load_w<NT>(P, S);
+        } else if (warp >= kMWarp0) {
+            if (lane == 0) gm_mma<NT, HALF, PER>(P, S, warp - kMWarp0);
+        } else if (P.x_bytes == 16) {
+            if (lane == 0) gm_load_x_tma<NT, PER>(P, S);
         } else if (P.x_bytes == 8) {
-            gm_load_x_any<NT, 8>(P, S, tid - 32 * kXWarp0);
+            gm_load_x_any<NT, PER, 8>(P, S, lane);
         } else if (P.x_bytes == 4) {
-            gm_load_x_any<NT, 4>(P, S, tid - 32 * kXWarp0);
+            gm_load_x_any<NT, PER, 4>(P, S, lane);
         } else {
-            gm_load_x_any<NT, 2>(P, S, tid - 32 * kXWarp0);
+            gm_load_x_any<NT, PER, 2>(P, S, lane);
         }
+        __syncwarp();
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 96;");
     } else if (warp < kSclWarp0) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsUnpack));
         gm_unpack<NT, HALF, PER>(P, S, warp - kUnpWarp0, lane);
+        __syncwarp();
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 96;");
     } else {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsScale));
         gm_scale<NT, HALF, PER>(P, S, warp - kSclWarp0, lane);
+        __syncwarp();
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 96;");
     }
     __syncwarp();
     if (P.split > 1) {
@@ -598,7 +685,7 @@ __global__ void __launch_bounds__(kQ4GemmThreads, 1)
     }
     tc_fence_before();
     __syncthreads();
-    if (warp == kMWarp) {
+    if (warp == kMWarp0) {
         tc_fence_after();
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(c.tmem_base),
                      "r"(512)
@@ -608,7 +695,7 @@ __global__ void __launch_bounds__(kQ4GemmThreads, 1)
 
 template <int NT>
 uint32_t gm_smem(uint32_t experts) {
-    return 1024 + x_ring<NT>() * NT * 256 + kWRing * kWStage + (sizeof(GmCtl) + 15) / 16 * 16 +
+    return 1024 + kSRing * NT * 256 + kWRing * kWStage + (sizeof(GmCtl) + 15) / 16 * 16 +
            (3 * experts + 1) * 4;
 }
 
