@@ -111,29 +111,41 @@ __device__ __forceinline__ float q4_scale(uint16_t bits, uint32_t half_scales) {
 // 128 + q in BF16, 1024 + q in FP16. Subtracting the pair of 2^m + z gives
 // q - z exactly: at most 4 significant bits.
 template <bool HALF>
-__device__ __forceinline__ uint32_t q4_magic() {
+__host__ __device__ constexpr uint32_t q4_magic() {
     return HALF ? 0x64006400u : 0x43004300u;
-}
-
-template <bool HALF>
-__device__ __forceinline__ uint32_t q4_sub2(uint32_t a, uint32_t b) {
-    uint32_t d;
-    if (HALF)
-        asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
-    else
-        asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
-    return d;
-}
-
-// The pair of elements 2 k and 2 k + 1 of a word as q - z.
-template <bool HALF>
-__device__ __forceinline__ uint32_t q4_pair(uint32_t word, int k, uint32_t zero_pair) {
-    return q4_sub2<HALF>(((word >> (4 * k)) & 0x000F000Fu) | q4_magic<HALF>(), zero_pair);
 }
 
 template <bool HALF>
 __device__ __forceinline__ uint32_t q4_zero_pair(uint32_t z) {
     return q4_magic<HALF>() | (z & 15u) * 0x00010001u;
+}
+
+// The masks of the unpacking, kept in registers: an instruction takes one
+// immediate, so with both as immediates (x & mask) | magic would be two.
+struct Q4Masks {
+    uint32_t mask, magic;
+    template <bool HALF>
+    static __device__ __forceinline__ Q4Masks make() {
+        Q4Masks m;
+        asm volatile("mov.u32 %0, %1;" : "=r"(m.mask) : "n"(0x000F000F));
+        asm volatile("mov.u32 %0, %1;" : "=r"(m.magic) : "n"(q4_magic<HALF>()));
+        return m;
+    }
+};
+
+// The pair of elements 2 k and 2 k + 1 of a word as q - z.
+template <bool HALF>
+__device__ __forceinline__ uint32_t q4_pair(uint32_t word, int k, uint32_t zero_pair,
+                                            const Q4Masks& m) {
+    uint32_t v, d;
+    asm("lop3.b32 %0, %1, %2, %3, 0xEA;"  // (a & b) | c
+        : "=r"(v)
+        : "r"(word >> (4 * k)), "r"(m.mask), "r"(m.magic));
+    if (HALF)
+        asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(v), "r"(zero_pair));
+    else
+        asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(v), "r"(zero_pair));
+    return d;
 }
 
 // ---------------------------------------------------------------------------

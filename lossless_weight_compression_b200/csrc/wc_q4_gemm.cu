@@ -140,17 +140,24 @@ __device__ __forceinline__ GmUnit unit_at(const GmParams& P, const GmSmem& S, ui
     return t;
 }
 
-__device__ __forceinline__ bool gm_wait(unsigned long long* bar, uint32_t parity, GmCtl& c,
-                                        int32_t* status, uint32_t sleep = 0) {
-    if (mbar_wait(bar, parity, &c.abort, sleep)) return true;
+// The wait's tail: the first poll (which suspends the thread for a while) ran out.
+__device__ __forceinline__ bool gm_wait_long(unsigned long long* bar, uint32_t parity, GmCtl& c,
+                                          int32_t* status) {
+    if (mbar_wait(bar, parity, &c.abort)) return true;
     if (!c.abort) report(status, kStatusTimeout);
     c.abort = 1;
     return false;
 }
 
+__device__ __forceinline__ bool gm_wait(unsigned long long* bar, uint32_t parity, GmCtl& c,
+                                        int32_t* status) {
+    if (mbar_try_wait(bar, parity)) return true;
+    return gm_wait_long(bar, parity, c, status);
+}
+
 __device__ __forceinline__ bool gm_wait_warp(unsigned long long* bar, uint32_t parity, GmCtl& c,
-                                             int32_t* status, uint32_t sleep = 0) {
-    return __all_sync(0xFFFFFFFFu, gm_wait(bar, parity, c, status, sleep));
+                                             int32_t* status) {
+    return __all_sync(0xFFFFFFFFu, gm_wait(bar, parity, c, status));
 }
 
 // A ring position: stage and how often the ring went round.
@@ -187,7 +194,7 @@ __device__ void gm_load_w(const GmParams& P, const GmSmem& S) {
         const uint32_t h = min(8u, L.blocks16 - 8 * t.rb);
         if (t.rb == 0 && s0 == 0) q4_check_header(stream, L, P.a.status);
         for (uint32_t s = s0; s < s1; ++s, w.next()) {
-            if (w.round > 0 && !gm_wait(&c.w_empty[w.s], w.empty(), c, P.a.status, 128)) {
+            if (w.round > 0 && !gm_wait(&c.w_empty[w.s], w.empty(), c, P.a.status)) {
                 ok = false;
                 break;
             }
@@ -216,7 +223,7 @@ __device__ void gm_load_x_tma(const GmParams& P, const GmSmem& S) {
         if (!t.valid) break;
         e = t.e;
         for (uint32_t s = s0; s < s1; ++s, x.next()) {
-            if (x.round > 0 && !gm_wait(&c.done[x.s][PER - 1], x.empty(), c, P.a.status, 128)) {
+            if (x.round > 0 && !gm_wait(&c.done[x.s][PER - 1], x.empty(), c, P.a.status)) {
                 ok = false;
                 break;
             }
@@ -255,7 +262,7 @@ __device__ void gm_load_x_any(const GmParams& P, const GmSmem& S, uint32_t tid) 
         if (!t.valid) break;
         e = t.e;
         for (uint32_t s = s0; s < s1; ++s, x.next()) {
-            if (x.round > 0 && !gm_wait_warp(&c.done[x.s][PER - 1], x.empty(), c, P.a.status, 128)) {
+            if (x.round > 0 && !gm_wait_warp(&c.done[x.s][PER - 1], x.empty(), c, P.a.status)) {
                 ok = false;
                 break;
             }
@@ -298,59 +305,66 @@ __device__ void gm_load_x_any(const GmParams& P, const GmSmem& S, uint32_t tid) 
     asm volatile("cp.async.wait_group 0;" ::: "memory");
 }
 
+// Slices of all the block's units.
+template <int NT>
+__device__ __forceinline__ uint32_t all_slices(const GmParams& P, const GmSmem& S) {
+    uint32_t s0, s1;
+    my_slices(P, s0, s1);
+    const uint32_t units = P.a.offsets == nullptr ? P.row_blocks * P.tiles : S.first[P.a.experts];
+    const uint32_t u0 = blockIdx.x / P.split, du = gridDim.x / P.split;
+    return u0 < units ? ((units - u0 + du - 1) / du) * (s1 - s0) : 0u;
+}
+
 // Unpacking warps 4..11: warps of parity k take the block's slices k, k + 2, ...
 template <int NT, bool HALF, int PER>
 __device__ void gm_unpack(const GmParams& P, const GmSmem& S, int wi, int lane) {
     GmCtl& c = *S.ctl;
     const Q4Layout& L = P.L;
+    const Q4Masks mk = Q4Masks::make<HALF>();
     const uint32_t q = uint32_t(wi) & 3u, turn = uint32_t(wi) >> 2;
     const uint32_t r = 32u * q + uint32_t(lane);
-    const uint32_t row_at = (r >> 4) * L.rec + (r & 15u) * 16u;
-    const uint32_t zero_at = (r >> 4) * L.rec + kQ4Codes + 32u * PER + (r & 15u);
+    const uint32_t row_at = smem_addr(S.w) + (r >> 4) * L.rec + (r & 15u) * 16u;
+    const uint32_t zero_at = smem_addr(S.w) + (r >> 4) * L.rec + kQ4Codes + 32u * PER + (r & 15u);
     const uint32_t t_lane = c.tmem_base + ((32u * q) << 16) + kACol;
-    uint32_t s0, s1, e = 0, count = 0;
-    my_slices(P, s0, s1);
-    Ring<kWRing> w;
-    Ring<kSRing> a;
-    for (uint32_t u = blockIdx.x / P.split;; u += gridDim.x / P.split) {
-        const GmUnit t = unit_at<NT>(P, S, u, e);
-        if (!t.valid) return;
-        e = t.e;
-        for (uint32_t s = s0; s < s1; ++s, ++count, w.next(), a.next()) {
-            if ((count & 1u) != turn) continue;
-            if (!gm_wait_warp(&c.w_full[w.s], w.full(), c, P.a.status)) return;
-            const uint32_t stage = smem_addr(S.w) + w.s * kWStage;
-            uint4 v[4];
-            uint32_t zp[PER];
+    const uint32_t total = all_slices<NT>(P, S);
+    const bool zeros = L.zeros != 0;
+    for (uint32_t n = turn; n < total; n += 2) {
+        const uint32_t ws = n % kWRing, st = n % kSRing;
+        if (!gm_wait_warp(&c.w_full[ws], (n / kWRing) & 1u, c, P.a.status)) return;
+        uint4 v[4];
+        uint32_t zp[PER];
 #pragma unroll
-            for (int k = 0; k < 4; ++k) v[k] = lds128(stage + row_at + 256u * k);
+        for (int k = 0; k < 4; ++k) v[k] = lds128(row_at + ws * kWStage + 256u * k);
 #pragma unroll
-            for (int k = 0; k < PER; ++k) {
-                uint32_t z = 8;
-                if (L.zeros)
-                    asm volatile("ld.shared.u8 %0, [%1];" : "=r"(z) : "r"(stage + zero_at + 16u * k));
-                zp[k] = q4_zero_pair<HALF>(z);
+        for (int k = 0; k < PER; ++k) {
+            uint32_t z = 8;
+            if (zeros)
+                asm volatile("ld.shared.u8 %0, [%1];"
+                             : "=r"(z)
+                             : "r"(zero_at + ws * kWStage + 16u * k));
+            zp[k] = q4_zero_pair<HALF>(z);
+        }
+        if (n >= kSRing &&
+            !gm_wait_warp(&c.done[st][PER - 1], (n / kSRing - 1u) & 1u, c, P.a.status))
+            return;
+        tc_fence_after();
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            uint32_t o[16];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const uint32_t word = i == 0 ? v[k].x : i == 1 ? v[k].y : i == 2 ? v[k].z : v[k].w;
+#pragma unroll
+                for (int p = 0; p < 4; ++p) o[4 * k + p] = q4_pair<HALF>(word, p, zp[i * PER / 4], mk);
             }
-            if (a.round > 0 && !gm_wait_warp(&c.done[a.s][PER - 1], a.empty(), c, P.a.status)) return;
-            tc_fence_after();
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                uint32_t o[16];
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    const uint32_t word = i == 0 ? v[k].x : i == 1 ? v[k].y : i == 2 ? v[k].z : v[k].w;
-#pragma unroll
-                    for (int p = 0; p < 4; ++p) o[4 * k + p] = q4_pair<HALF>(word, p, zp[i * PER / 4]);
-                }
-                tmem_st16(t_lane + a.s * 64u + 16u * i, o);
-            }
-            tmem_wait_st();
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) {
-                mbar_arrive(&c.w_empty[w.s]);
-                mbar_arrive(&c.s_full[a.s]);
-            }
+            tmem_st16(t_lane + st * 64u + 16u * i, o);
+        }
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) {
+            mbar_arrive(&c.w_empty[ws]);
+            mbar_arrive(&c.s_full[st]);
         }
     }
 }
@@ -371,12 +385,12 @@ __device__ void gm_mma(const GmParams& P, const GmSmem& S, uint32_t turn) {
         if (!t.valid) break;
         e = t.e;
         // kind::f16: FP32 accumulator, A and B both BF16 or both FP16 (0 in bits 7-12)
-        const uint32_t n = (t.ntok + 15u) & ~15u;
-        const uint32_t idesc = HALF ? bf16_idesc(kRowsTile, n) & ~((1u << 7) | (1u << 10))
-                                    : bf16_idesc(kRowsTile, n);
-        for (uint32_t s = s0; ok && s < s1; ++s, ++count) {
-            if (count % kMWarps != turn) continue;
-            const uint32_t st = count % kSRing, round = count / kSRing;
+        const uint32_t nn = (t.ntok + 15u) & ~15u;
+        const uint32_t idesc = HALF ? bf16_idesc(kRowsTile, nn) & ~((1u << 7) | (1u << 10))
+                                    : bf16_idesc(kRowsTile, nn);
+        const uint32_t end = count + (s1 - s0);
+        for (uint32_t n = count + ((count ^ turn) & 1u); ok && n < end; n += kMWarps) {
+            const uint32_t st = n % kSRing, round = n / kSRing;
             const uint32_t ta = c.tmem_base + kACol + st * 64u;
             const uint64_t xd0 = sw128_desc(x0 + st * (NT * 256));
             const uint64_t xd1 = xd0 + NT * 8;
@@ -386,8 +400,8 @@ __device__ void gm_mma(const GmParams& P, const GmSmem& S, uint32_t turn) {
             }
             // The accumulator ring is waited for in order: a thread that came
             // to it a slice early would take an older phase for its own.
-            if (!A::by_slice && count > 0 &&
-                !gm_wait(&c.order[turn], ((count - 1) / kMWarps) & 1u, c, P.a.status)) {
+            if (!A::by_slice && n > 0 &&
+                !gm_wait(&c.order[turn], ((n - 1) / kMWarps) & 1u, c, P.a.status)) {
                 ok = false;
                 break;
             }
@@ -396,9 +410,9 @@ __device__ void gm_mma(const GmParams& P, const GmSmem& S, uint32_t turn) {
             for (int g = 0; g < PER; ++g) {
                 uint32_t d;
                 if (A::by_slice) {
-                    d = (count % A::slices) * PER + g;
+                    d = (n % A::slices) * PER + g;
                 } else {
-                    const uint32_t gi = count * PER + g;
+                    const uint32_t gi = n * PER + g;
                     d = gi % A::ring;
                     if (gi / A::ring > 0 &&
                         !gm_wait(&c.acc_empty[d], (gi / A::ring - 1u) & 1u, c, P.a.status)) {
@@ -419,6 +433,7 @@ __device__ void gm_mma(const GmParams& P, const GmSmem& S, uint32_t turn) {
                 umma_commit(&c.done[st][g]);
             }
         }
+        count = end;
     }
     if (issued) {  // every MMA has finished before the block ends
         umma_commit(&c.drain[turn]);
@@ -490,11 +505,11 @@ __device__ void gm_scale(const GmParams& P, const GmSmem& S, int wi, int lane) {
     constexpr int HN = NT / 2;  // columns of this warp
     const uint32_t q = uint32_t(wi) & 3u, half = uint32_t(wi) >> 2;
     const uint32_t r = 32u * q + uint32_t(lane);
-    const uint32_t scale_at = (r >> 4) * L.rec + kQ4Codes + (r & 15u) * 2u;
+    const uint32_t scale_at = smem_addr(S.w) + (r >> 4) * L.rec + kQ4Codes + (r & 15u) * 2u;
+    const uint32_t half_scales = L.half_scales;
     const uint32_t t_lane = c.tmem_base + ((32u * q) << 16) + half * HN;
     uint32_t s0, s1, e = 0, count = 0;
     my_slices(P, s0, s1);
-    Ring<kWRing> w;
     if (A::by_slice && lane == 0)  // the first slices' accumulators are free
         for (uint32_t k = 0; k < A::slices; ++k) mbar_arrive(&c.s_full[k]);
     for (uint32_t u = blockIdx.x / P.split;; u += gridDim.x / P.split) {
@@ -505,25 +520,25 @@ __device__ void gm_scale(const GmParams& P, const GmSmem& S, int wi, int lane) {
 #pragma unroll
         for (int k = 0; k < HN / 2; ++k) sum[k] = make_float2(0.f, 0.f);
         const uint32_t live = t.ntok > half * HN ? t.ntok - half * HN : 0u;  // columns in use
-        for (uint32_t s = s0; s < s1; ++s, ++count, w.next()) {
-            const uint32_t st = count % kSRing, round = count / kSRing;
-            if (!gm_wait_warp(&c.w_full[w.s], w.full(), c, P.a.status, 64)) return;
+        for (const uint32_t end = count + (s1 - s0); count < end; ++count) {
+            const uint32_t st = count % kSRing, round = count / kSRing, ws = count % kWRing;
+            if (!gm_wait_warp(&c.w_full[ws], (count / kWRing) & 1u, c, P.a.status)) return;
             float sc[PER];
 #pragma unroll
             for (int g = 0; g < PER; ++g) {
                 uint16_t b;
                 asm volatile("ld.shared.u16 %0, [%1];"
                              : "=h"(b)
-                             : "r"(smem_addr(S.w) + w.s * kWStage + scale_at + 32u * g));
-                sc[g] = q4_scale(b, L.half_scales);
+                             : "r"(scale_at + ws * kWStage + 32u * g));
+                sc[g] = q4_scale(b, half_scales);
             }
             __syncwarp();
-            if (lane == 0) mbar_arrive(&c.w_empty[w.s]);
+            if (lane == 0) mbar_arrive(&c.w_empty[ws]);
 #pragma unroll
             for (int g = 0; g < PER; ++g) {
                 const uint32_t gi = count * PER + g;
                 const uint32_t d = A::by_slice ? (count % A::slices) * PER + g : gi % A::ring;
-                if (!gm_wait_warp(&c.done[st][g], round & 1u, c, P.a.status, 64)) return;
+                if (!gm_wait_warp(&c.done[st][g], round & 1u, c, P.a.status)) return;
                 tc_fence_after();
                 if (live > 0) {
                     uint32_t v[HN];
@@ -651,17 +666,17 @@ __global__ void __launch_bounds__(kQ4GemmThreads, 1)
         } else {
             gm_load_x_any<NT, PER, 2>(P, S, lane);
         }
-        __syncwarp();
+        __syncthreads();  // (no warp spins for the registers that the scaling warps hold)
         asm volatile("setmaxnreg.inc.sync.aligned.u32 96;");
     } else if (warp < kSclWarp0) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsUnpack));
         gm_unpack<NT, HALF, PER>(P, S, warp - kUnpWarp0, lane);
-        __syncwarp();
+        __syncthreads();
         asm volatile("setmaxnreg.inc.sync.aligned.u32 96;");
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsScale));
         gm_scale<NT, HALF, PER>(P, S, warp - kSclWarp0, lane);
-        __syncwarp();
+        __syncthreads();
         asm volatile("setmaxnreg.dec.sync.aligned.u32 96;");
     }
     __syncwarp();

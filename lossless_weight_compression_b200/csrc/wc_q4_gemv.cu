@@ -66,6 +66,7 @@ __device__ __forceinline__ void slice_mma(const uint4 (&c0)[RT], const uint4 (&c
                                           const uint16_t (&s0)[RT][PER], const uint16_t (&s1)[RT][PER],
                                           const uint32_t (&z0)[RT][PER], const uint32_t (&z1)[RT][PER],
                                           const uint4 (&xv)[NT][4], uint32_t half_scales,
+                                          const Q4Masks& mk,
                                           float (&acc)[RT][NT][4]) {
 #pragma unroll
     for (int g = 0; g < PER; ++g) {
@@ -83,10 +84,10 @@ __device__ __forceinline__ void slice_mma(const uint4 (&c0)[RT], const uint4 (&c
                 const uint32_t w0 = word_of(c0[r], i), w1 = word_of(c1[r], i);
 #pragma unroll
                 for (int m = 0; m < 2; ++m) {
-                    const uint32_t a0 = q4_pair<HALF>(w0, 2 * m, z0[r][g]);
-                    const uint32_t a1 = q4_pair<HALF>(w1, 2 * m, z1[r][g]);
-                    const uint32_t a2 = q4_pair<HALF>(w0, 2 * m + 1, z0[r][g]);
-                    const uint32_t a3 = q4_pair<HALF>(w1, 2 * m + 1, z1[r][g]);
+                    const uint32_t a0 = q4_pair<HALF>(w0, 2 * m, z0[r][g], mk);
+                    const uint32_t a1 = q4_pair<HALF>(w1, 2 * m, z1[r][g], mk);
+                    const uint32_t a2 = q4_pair<HALF>(w0, 2 * m + 1, z0[r][g], mk);
+                    const uint32_t a3 = q4_pair<HALF>(w1, 2 * m + 1, z1[r][g], mk);
 #pragma unroll
                     for (int n = 0; n < NT; ++n)
                         mma16816<HALF>(part[r][n], a0, a1, a2, a3, word_of(xv[n][i], 2 * m),
@@ -126,6 +127,7 @@ __global__ void __launch_bounds__(kGvThreads) q4_gemv_kernel(const __grid_consta
     const uint8_t* stream = A.stream + e * A.stride;
     if (blockIdx.x == 0 && threadIdx.x == 0 && hi > lo) q4_check_header(stream, L, A.status);
     const uint32_t h = min(8u, L.blocks16 - (b0 & ~7u));
+    const Q4Masks mk = Q4Masks::make<HALF>();
     const uint32_t nrec = min(uint32_t(RT), L.blocks16 - b0);
     for (uint32_t t0 = lo; t0 < hi; t0 += 8 * NT) {
         float acc[RT][NT][4] = {};
@@ -158,7 +160,7 @@ __global__ void __launch_bounds__(kGvThreads) q4_gemv_kernel(const __grid_consta
                     xv[n][i] = tok < hi ? load_x8(row, s * kQ4Cols + 32 * i + 8 * t, L.cols, P.vec)
                                         : make_uint4(0, 0, 0, 0);
             }
-            slice_mma<HALF, RT, NT, PER>(c0, c1, s0, s1, z0, z1, xv, L.half_scales, acc);
+            slice_mma<HALF, RT, NT, PER>(c0, c1, s0, s1, z0, z1, xv, L.half_scales, mk, acc);
         }
         // partial sums of the block's warps, then of the cluster's blocks, in a fixed order
 #pragma unroll
