@@ -140,19 +140,50 @@ __device__ __forceinline__ GmUnit unit_at(const GmParams& P, const GmSmem& S, ui
     return t;
 }
 
-// The wait's tail: the first poll (which suspends the thread for a while) ran out.
-__device__ __forceinline__ bool gm_wait_long(unsigned long long* bar, uint32_t parity, GmCtl& c,
-                                          int32_t* status) {
-    if (mbar_wait(bar, parity, &c.abort)) return true;
-    if (!c.abort) report(status, kStatusTimeout);
-    c.abort = 1;
-    return false;
+// One poll, which suspends the thread for a while. Without a time of its own: a
+// poll that names one becomes a loop of polls, sleeps and clock reads (measured
+// here: 350 barrier and 160 sleep instructions a slice instead of some 75), whose
+// instructions the other roles wait for.
+__device__ __forceinline__ bool gm_poll(unsigned long long* bar, uint32_t parity) {
+    uint32_t done;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(done)
+        : "r"(smem_addr(bar)), "r"(parity)
+        : "memory");
+    return done != 0;
 }
 
+// Wait for a phase; false if another role gave up or the time limit passed.
 __device__ __forceinline__ bool gm_wait(unsigned long long* bar, uint32_t parity, GmCtl& c,
                                         int32_t* status) {
-    if (mbar_try_wait(bar, parity)) return true;
-    return gm_wait_long(bar, parity, c, status);
+    uint64_t t0 = 0;
+    for (;;) {
+#pragma unroll 1
+        for (int k = 0; k < 256; ++k)
+            if (gm_poll(bar, parity)) return true;
+        const uint64_t t = global_timer_ns();
+        if (t0 == 0) t0 = t;
+        if (*const_cast<volatile int*>(&c.abort)) return false;
+        if (t - t0 > kWaitLimitNs) {
+            report(status, kStatusTimeout);
+            c.abort = 1;
+            return false;
+        }
+    }
+}
+
+// True in one lane of the (converged) warp.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t e;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t.reg .b32 l;\n\t"
+        "elect.sync l|p, 0xFFFFFFFF;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(e));
+    return e != 0;
 }
 
 __device__ __forceinline__ bool gm_wait_warp(unsigned long long* bar, uint32_t parity, GmCtl& c,
@@ -305,6 +336,12 @@ __device__ void gm_load_x_any(const GmParams& P, const GmSmem& S, uint32_t tid) 
     asm volatile("cp.async.wait_group 0;" ::: "memory");
 }
 
+__device__ __forceinline__ void tmem_st4(uint32_t taddr, const uint32_t (&v)[4]) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%0], {%1,%2,%3,%4};" ::"r"(taddr),
+                 "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3])
+                 : "memory");
+}
+
 // Slices of all the block's units.
 template <int NT>
 __device__ __forceinline__ uint32_t all_slices(const GmParams& P, const GmSmem& S) {
@@ -331,10 +368,7 @@ __device__ void gm_unpack(const GmParams& P, const GmSmem& S, int wi, int lane) 
     for (uint32_t n = turn; n < total; n += 2) {
         const uint32_t ws = n % kWRing, st = n % kSRing;
         if (!gm_wait_warp(&c.w_full[ws], (n / kWRing) & 1u, c, P.a.status)) return;
-        uint4 v[4];
         uint32_t zp[PER];
-#pragma unroll
-        for (int k = 0; k < 4; ++k) v[k] = lds128(row_at + ws * kWStage + 256u * k);
 #pragma unroll
         for (int k = 0; k < PER; ++k) {
             uint32_t z = 8;
@@ -348,16 +382,19 @@ __device__ void gm_unpack(const GmParams& P, const GmSmem& S, int wi, int lane) 
             !gm_wait_warp(&c.done[st][PER - 1], (n / kSRing - 1u) & 1u, c, P.a.status))
             return;
         tc_fence_after();
+        // not unrolled: the roles share an instruction cache
+        uint32_t src = row_at + ws * kWStage, dst = t_lane + st * 64u;
+#pragma unroll 1
+        for (int k = 0; k < 4; ++k, src += 256u, dst += 4u) {
+            const uint4 v = lds128(src);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            uint32_t o[16];
+            for (int i = 0; i < 4; ++i) {
+                const uint32_t word = i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w;
+                uint32_t o[4];
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                const uint32_t word = i == 0 ? v[k].x : i == 1 ? v[k].y : i == 2 ? v[k].z : v[k].w;
-#pragma unroll
-                for (int p = 0; p < 4; ++p) o[4 * k + p] = q4_pair<HALF>(word, p, zp[i * PER / 4], mk);
+                for (int p = 0; p < 4; ++p) o[p] = q4_pair<HALF>(word, p, zp[i * PER / 4], mk);
+                tmem_st4(dst + 16u * i, o);
             }
-            tmem_st16(t_lane + st * 64u + 16u * i, o);
         }
         tmem_wait_st();
         tc_fence_before();
@@ -369,9 +406,10 @@ __device__ void gm_unpack(const GmParams& P, const GmSmem& S, int wi, int lane) 
     }
 }
 
-// Issue of the block's slices k, k + 2, ... (k = turn): what a thread does
+// Issue of the block's slices k, k + 2, ... (k = turn): what a warp does
 // between two slices' MMAs (some 300 cycles of waits and commits beside their
-// 400 to 500) overlaps the other's.
+// 400 to 500) overlaps the other's. The whole warp walks, so that addresses and
+// descriptors stay in uniform registers; one lane issues.
 template <int NT, bool HALF, int PER>
 __device__ void gm_mma(const GmParams& P, const GmSmem& S, uint32_t turn) {
     GmCtl& c = *S.ctl;
@@ -394,14 +432,14 @@ __device__ void gm_mma(const GmParams& P, const GmSmem& S, uint32_t turn) {
             const uint32_t ta = c.tmem_base + kACol + st * 64u;
             const uint64_t xd0 = sw128_desc(x0 + st * (NT * 256));
             const uint64_t xd1 = xd0 + NT * 8;
-            if (!gm_wait(&c.s_full[st], round & 1u, c, P.a.status)) {
+            if (!gm_wait_warp(&c.s_full[st], round & 1u, c, P.a.status)) {
                 ok = false;
                 break;
             }
             // The accumulator ring is waited for in order: a thread that came
             // to it a slice early would take an older phase for its own.
             if (!A::by_slice && n > 0 &&
-                !gm_wait(&c.order[turn], ((n - 1) / kMWarps) & 1u, c, P.a.status)) {
+                !gm_wait_warp(&c.order[turn], ((n - 1) / kMWarps) & 1u, c, P.a.status)) {
                 ok = false;
                 break;
             }
@@ -415,28 +453,32 @@ __device__ void gm_mma(const GmParams& P, const GmSmem& S, uint32_t turn) {
                     const uint32_t gi = n * PER + g;
                     d = gi % A::ring;
                     if (gi / A::ring > 0 &&
-                        !gm_wait(&c.acc_empty[d], (gi / A::ring - 1u) & 1u, c, P.a.status)) {
+                        !gm_wait_warp(&c.acc_empty[d], (gi / A::ring - 1u) & 1u, c, P.a.status)) {
                         ok = false;
                         break;
                     }
                     tc_fence_after();
                 }
                 const uint32_t acc = c.tmem_base + d * NT;
+if (elect_one()) {
 #pragma unroll
-                for (int k = 0; k < 8 / PER; ++k) {
-                    const int kk = g * (8 / PER) + k;
-                    umma_bf16_ts(acc, ta + 8u * kk, (kk < 4 ? xd0 : xd1) + 2u * (kk & 3), idesc,
-                                 k > 0 ? 1u : 0u);
+                    for (int k = 0; k < 8 / PER; ++k) {
+                        const int kk = g * (8 / PER) + k;
+                        umma_bf16_ts(acc, ta + 8u * kk, (kk < 4 ? xd0 : xd1) + 2u * (kk & 3), idesc,
+                                     k > 0 ? 1u : 0u);
+                    }
+                    if (!A::by_slice && g == PER - 1) mbar_arrive(&c.order[turn ^ 1u]);
+                    umma_commit(&c.done[st][g]);
                 }
+                __syncwarp();
                 issued = true;
-                if (!A::by_slice && g == PER - 1) mbar_arrive(&c.order[turn ^ 1u]);
-                umma_commit(&c.done[st][g]);
             }
         }
         count = end;
     }
-    if (issued) {  // every MMA has finished before the block ends
-        umma_commit(&c.drain[turn]);
+    if (issued) {  // every MMA has finished before the block ends (issued by this lane: elect.sync
+                   // picks the same one each time)
+        if (elect_one()) umma_commit(&c.drain[turn]);
         mbar_wait(&c.drain[turn], 0, nullptr);
     }
 }
@@ -581,7 +623,8 @@ template <int NT, bool HALF, int PER>
 __global__ void __launch_bounds__(kQ4GemmThreads, 1)
     q4_gemm_kernel(const __grid_constant__ GmParams P) {
     extern __shared__ __align__(1024) unsigned char smem_raw[];
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int tid = threadIdx.x, lane = tid & 31;
+    const int warp = __shfl_sync(0xFFFFFFFFu, tid >> 5, 0);  // uniform
     uint8_t* p = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
     GmSmem S;
     S.x = p;
@@ -656,7 +699,7 @@ __global__ void __launch_bounds__(kQ4GemmThreads, 1)
         if (warp == kWWarp) {
             if (lane == 0) gm_load_w<NT>(P, S);
         } else if (warp >= kMWarp0) {
-            if (lane == 0) gm_mma<NT, HALF, PER>(P, S, warp - kMWarp0);
+            gm_mma<NT, HALF, PER>(P, S, warp - kMWarp0);
         } else if (P.x_bytes == 16) {
             if (lane == 0) gm_load_x_tma<NT, PER>(P, S);
         } else if (P.x_bytes == 8) {
