@@ -11,12 +11,12 @@
 //     loads the slice's activations by TMA in the 128-byte swizzled K-major
 //     layout the MMA reads B in (two warps with narrower copies when the rows
 //     of x are not 16-byte aligned);
-//   - eight unpacking warps, four per slice in turns, one lane per row, turn
+//   - twelve unpacking warps, four per slice in turns, one lane per row, turn
 //     codes into 16-bit integers q - z and store them as the A operand into
 //     tensor memory;
-//   - two threads issue tcgen05.mma for slices in turns, each GROUP of columns
-//     into an accumulator of its own in tensor memory: the products are exact
-//     and a group sums at most 128 of them;
+//   - two warps issue tcgen05.mma, each GROUP of columns into an accumulator
+//     of its own in tensor memory: the products are exact and a group sums at
+//     most 128 of them;
 //   - eight scaling warps read a group's accumulator (tcgen05.ld), scale it in
 //     FP32 and add it to the row's sums in registers.
 // Scaling sums instead of weights keeps every weight exact (s (q - z) has up to
@@ -47,29 +47,25 @@ constexpr uint32_t kMaxRecBytes = kQ4Codes + 32u * 4u + 64u;
 constexpr uint32_t kWStage = 8 * kMaxRecBytes;
 constexpr uint32_t kSmemMax = 232448;
 
-constexpr int kWWarp = 0, kMWarp0 = 2;  // 1: activations; 2, 3: MMA issue, slices in turns
 constexpr int kMWarps = 2;
-constexpr int kUnpWarp0 = 4;   // 4..11: lane quarter warp % 4, slices of its parity
-constexpr int kSclWarp0 = 12;  // 12..19: lane quarter warp % 4, half of the columns
+constexpr int kWWarp = 0, kMWarp0 = 2;  // 1: activations; 2, 3: MMA issue
+constexpr int kUnpWarp0 = 4;    // 4..15: lane quarter warp % 4, slices in turns of three
+constexpr int kUnpTurns = 3;
+constexpr int kSclWarp0 = 16;   // 16..23: lane quarter warp % 4, half of the columns
 constexpr int kSclWarps = 8;
-constexpr int kQ4GemmThreads = 32 * 20;
+constexpr int kQ4GemmThreads = 32 * 24;
 
-// Registers of a thread after the roles split (of 96 at launch: 4 x 48 +
-// 8 x 64 + 8 x 152 warps = 20 x 96): a scaling warp holds up to 64 sums and as
-// many results on their way.
-constexpr int kRegsIssue = 48, kRegsUnpack = 64, kRegsScale = 152;
-static_assert(4 * kRegsIssue + 8 * kRegsUnpack + 8 * kRegsScale == 20 * 96, "register split");
+// Registers of a thread after the roles split (of 80 at launch: (4 + 12) x 48 +
+// 8 x 144 warps = 24 x 80): a scaling warp holds up to 64 sums and as many
+// results on their way.
+constexpr int kRegsLaunch = 80, kRegsIssue = 48, kRegsUnpack = 48, kRegsScale = 144;
+static_assert(4 * kRegsIssue + 12 * kRegsUnpack + 8 * kRegsScale == 24 * kRegsLaunch, "registers");
 
-// Accumulators of NT columns. Where they hold two slices' groups or more, the
-// scaling warps' word that a slice's accumulators are free is one more arrival
-// on the barrier that hands its operands over (an issuing thread's every wait
-// delays its next MMA); else the groups go round a ring with barriers of its own.
+// Accumulators of NT columns: group number n of the block goes to n % accs.
 template <int NT, int PER>
-struct Acc {
-    static constexpr uint32_t ring = kAccCols / NT;
-    static constexpr bool by_slice = ring >= 2 * PER;
-    static constexpr uint32_t slices = by_slice ? (ring / PER > kSRing ? kSRing : ring / PER) : 1;
-};
+__host__ __device__ constexpr uint32_t accs() {
+    return kAccCols / NT < kSRing * PER ? kAccCols / NT : kSRing * PER;
+}
 
 struct GmParams {
     CUtensorMap x_map;
@@ -84,10 +80,13 @@ struct GmParams {
 
 struct GmCtl {
     unsigned long long w_full[kWRing], w_empty[kWRing];
-    unsigned long long s_full[kSRing];     // x and A of a slice (and free accumulators)
-    unsigned long long done[kSRing][4];    // the MMAs of a slice's groups
-    unsigned long long acc_empty[4];       // !by_slice: accumulator ring,
-    unsigned long long order[kMWarps];     //   and the issuing threads' turns at it
+    // A group's operands and a free accumulator: the one thing its issue waits
+    // for. Arrivals: the unpacking warps; the scaling warps, when they have read
+    // the accumulator's last group; and the activations' copy, on the first
+    // group of each 64-column panel.
+    unsigned long long g_full[kSRing][4];
+    unsigned long long done[kSRing][4];    // the MMAs of a group
+    unsigned long long s_free[kSRing];     // the MMAs of a slice (PER > 1: of both issuing warps)
     unsigned long long drain[kMWarps];
     uint32_t tmem_base;
     int abort;
@@ -156,9 +155,11 @@ __device__ __forceinline__ bool gm_poll(unsigned long long* bar, uint32_t parity
     return done != 0;
 }
 
-// Wait for a phase; false if another role gave up or the time limit passed.
-__device__ __forceinline__ bool gm_wait(unsigned long long* bar, uint32_t parity, GmCtl& c,
-                                        int32_t* status) {
+// Wait for a phase; false if another role gave up or the time limit passed. The
+// rare part stays out of the way of the instructions that follow a poll which
+// succeeds at once.
+__device__ __forceinline__ bool gm_wait_more(unsigned long long* bar, uint32_t parity, GmCtl& c,
+                                             int32_t* status) {
     uint64_t t0 = 0;
     for (;;) {
 #pragma unroll 1
@@ -175,6 +176,12 @@ __device__ __forceinline__ bool gm_wait(unsigned long long* bar, uint32_t parity
     }
 }
 
+__device__ __forceinline__ bool gm_wait(unsigned long long* bar, uint32_t parity, GmCtl& c,
+                                        int32_t* status) {
+    if (__builtin_expect(gm_poll(bar, parity), 1)) return true;
+    return gm_wait_more(bar, parity, c, status);
+}
+
 // True in one lane of the (converged) warp.
 __device__ __forceinline__ bool elect_one() {
     uint32_t e;
@@ -186,9 +193,12 @@ __device__ __forceinline__ bool elect_one() {
     return e != 0;
 }
 
+// The same by a whole warp: if any lane gives up, all do, so that the warp stays
+// converged for its warp-wide tcgen05 instructions.
 __device__ __forceinline__ bool gm_wait_warp(unsigned long long* bar, uint32_t parity, GmCtl& c,
                                              int32_t* status) {
-    return __all_sync(0xFFFFFFFFu, gm_wait(bar, parity, c, status));
+    if (__builtin_expect(__all_sync(0xFFFFFFFFu, gm_poll(bar, parity)), 1)) return true;
+    return __all_sync(0xFFFFFFFFu, gm_wait_more(bar, parity, c, status));
 }
 
 // A ring position: stage and how often the ring went round.
@@ -254,21 +264,26 @@ __device__ void gm_load_x_tma(const GmParams& P, const GmSmem& S) {
         if (!t.valid) break;
         e = t.e;
         for (uint32_t s = s0; s < s1; ++s, x.next()) {
-            if (x.round > 0 && !gm_wait(&c.done[x.s][PER - 1], x.empty(), c, P.a.status)) {
+            if (x.round > 0 && !gm_wait(&c.s_free[x.s], x.empty(), c, P.a.status)) {
                 ok = false;
                 break;
             }
             uint8_t* d = S.x + x.s * NT * 256;
-            mbar_arrive_expect_tx(&c.s_full[x.s], NT * 256);
-            tma_load_2d(d, &P.x_map, int32_t(s * kQ4Cols), int32_t(t.tok0), &c.s_full[x.s]);
-            tma_load_2d(d + NT * 128, &P.x_map, int32_t(s * kQ4Cols + 64), int32_t(t.tok0),
-                        &c.s_full[x.s]);
+            unsigned long long* b0 = &c.g_full[x.s][0];
+            unsigned long long* b1 = &c.g_full[x.s][PER / 2];
+            mbar_arrive_expect_tx(b0, NT * (PER == 1 ? 256 : 128));
+            tma_load_2d(d, &P.x_map, int32_t(s * kQ4Cols), int32_t(t.tok0), b0);
+            if (PER > 1) mbar_arrive_expect_tx(b1, NT * 128);
+            tma_load_2d(d + NT * 128, &P.x_map, int32_t(s * kQ4Cols + 64), int32_t(t.tok0), b1);
         }
     }
     if (!ok) {  // (bounded: an aborted slice's other arrivals may never come)
         for (uint32_t k = 0; k < kSRing; ++k) {
             const uint32_t r = k < x.s ? x.round : x.round - 1u;
-            if (k < x.s || x.round > 0) mbar_wait(&c.s_full[k], r & 1u, nullptr);
+            if (k < x.s || x.round > 0) {
+                mbar_wait(&c.g_full[k][0], r & 1u, nullptr);
+                mbar_wait(&c.g_full[k][PER / 2], r & 1u, nullptr);
+            }
         }
     }
 }
@@ -285,7 +300,8 @@ __device__ void gm_load_x_any(const GmParams& P, const GmSmem& S, uint32_t tid) 
     int prev = -1;  // stage not yet handed over
     auto hand_over = [&](int stage) {
         fence_proxy_async_smem();
-        mbar_arrive(&c.s_full[stage]);
+        mbar_arrive(&c.g_full[stage][0]);
+        if (PER > 1) mbar_arrive(&c.g_full[stage][PER / 2]);
     };
     bool ok = true;
     for (uint32_t u = blockIdx.x / P.split; ok; u += gridDim.x / P.split) {
@@ -293,7 +309,7 @@ __device__ void gm_load_x_any(const GmParams& P, const GmSmem& S, uint32_t tid) 
         if (!t.valid) break;
         e = t.e;
         for (uint32_t s = s0; s < s1; ++s, x.next()) {
-            if (x.round > 0 && !gm_wait_warp(&c.done[x.s][PER - 1], x.empty(), c, P.a.status)) {
+            if (x.round > 0 && !gm_wait_warp(&c.s_free[x.s], x.empty(), c, P.a.status)) {
                 ok = false;
                 break;
             }
@@ -352,7 +368,7 @@ __device__ __forceinline__ uint32_t all_slices(const GmParams& P, const GmSmem& 
     return u0 < units ? ((units - u0 + du - 1) / du) * (s1 - s0) : 0u;
 }
 
-// Unpacking warps 4..11: warps of parity k take the block's slices k, k + 2, ...
+// Unpacking warps: four a slice, the block's slices in turns.
 template <int NT, bool HALF, int PER>
 __device__ void gm_unpack(const GmParams& P, const GmSmem& S, int wi, int lane) {
     GmCtl& c = *S.ctl;
@@ -365,7 +381,7 @@ __device__ void gm_unpack(const GmParams& P, const GmSmem& S, int wi, int lane) 
     const uint32_t t_lane = c.tmem_base + ((32u * q) << 16) + kACol;
     const uint32_t total = all_slices<NT>(P, S);
     const bool zeros = L.zeros != 0;
-    for (uint32_t n = turn; n < total; n += 2) {
+    for (uint32_t n = turn; n < total; n += kUnpTurns) {
         const uint32_t ws = n % kWRing, st = n % kSRing;
         if (!gm_wait_warp(&c.w_full[ws], (n / kWRing) & 1u, c, P.a.status)) return;
         uint32_t zp[PER];
@@ -379,7 +395,7 @@ __device__ void gm_unpack(const GmParams& P, const GmSmem& S, int wi, int lane) 
             zp[k] = q4_zero_pair<HALF>(z);
         }
         if (n >= kSRing &&
-            !gm_wait_warp(&c.done[st][PER - 1], (n / kSRing - 1u) & 1u, c, P.a.status))
+            !gm_wait_warp(&c.s_free[st], (n / kSRing - 1u) & 1u, c, P.a.status))
             return;
         tc_fence_after();
         // not unrolled: the roles share an instruction cache
@@ -400,20 +416,26 @@ __device__ void gm_unpack(const GmParams& P, const GmSmem& S, int wi, int lane) 
         tc_fence_before();
         __syncwarp();
         if (lane == 0) {
+#pragma unroll
+            for (int g = 0; g < PER; ++g) mbar_arrive(&c.g_full[st][g]);
             mbar_arrive(&c.w_empty[ws]);
-            mbar_arrive(&c.s_full[st]);
         }
     }
 }
 
-// Issue of the block's slices k, k + 2, ... (k = turn): what a warp does
-// between two slices' MMAs (some 300 cycles of waits and commits beside their
-// 400 to 500) overlaps the other's. The whole warp walks, so that addresses and
-// descriptors stay in uniform registers; one lane issues.
+// MMA issue. One group a slice: the two warps take slices in turns; more: warp
+// p takes the groups of the 64-column panel p of every slice. A warp's next
+// wait returns only after the MMAs it issued before have left its queue (a
+// barrier poll or any other read of shared memory behind 8 of them costs some
+// 170 cycles), so there is one wait a group and the other warp's MMAs run
+// meanwhile. The whole warp walks, so that addresses and descriptors stay in
+// uniform registers; one lane issues.
 template <int NT, bool HALF, int PER>
 __device__ void gm_mma(const GmParams& P, const GmSmem& S, uint32_t turn) {
     GmCtl& c = *S.ctl;
-    using A = Acc<NT, PER>;
+    constexpr uint32_t ACCS = accs<NT, PER>();
+    constexpr int kGroups = PER == 1 ? 1 : PER / 2;  // of this warp in a slice it takes
+    constexpr int kMmas = 8 / PER;                   // a group
     const uint32_t x0 = smem_addr(S.x);
     uint32_t s0, s1, e = 0, count = 0;
     my_slices(P, s0, s1);
@@ -427,48 +449,32 @@ __device__ void gm_mma(const GmParams& P, const GmSmem& S, uint32_t turn) {
         const uint32_t idesc = HALF ? bf16_idesc(kRowsTile, nn) & ~((1u << 7) | (1u << 10))
                                     : bf16_idesc(kRowsTile, nn);
         const uint32_t end = count + (s1 - s0);
-        for (uint32_t n = count + ((count ^ turn) & 1u); ok && n < end; n += kMWarps) {
+        for (uint32_t n = PER == 1 ? count + ((count ^ turn) & 1u) : count; ok && n < end;
+             n += PER == 1 ? kMWarps : 1) {
             const uint32_t st = n % kSRing, round = n / kSRing;
             const uint32_t ta = c.tmem_base + kACol + st * 64u;
             const uint64_t xd0 = sw128_desc(x0 + st * (NT * 256));
             const uint64_t xd1 = xd0 + NT * 8;
-            if (!gm_wait_warp(&c.s_full[st], round & 1u, c, P.a.status)) {
-                ok = false;
-                break;
-            }
-            // The accumulator ring is waited for in order: a thread that came
-            // to it a slice early would take an older phase for its own.
-            if (!A::by_slice && n > 0 &&
-                !gm_wait_warp(&c.order[turn], ((n - 1) / kMWarps) & 1u, c, P.a.status)) {
-                ok = false;
-                break;
-            }
-            tc_fence_after();
 #pragma unroll
-            for (int g = 0; g < PER; ++g) {
-                uint32_t d;
-                if (A::by_slice) {
-                    d = (n % A::slices) * PER + g;
-                } else {
-                    const uint32_t gi = n * PER + g;
-                    d = gi % A::ring;
-                    if (gi / A::ring > 0 &&
-                        !gm_wait_warp(&c.acc_empty[d], (gi / A::ring - 1u) & 1u, c, P.a.status)) {
-                        ok = false;
-                        break;
-                    }
-                    tc_fence_after();
+            for (int j = 0; j < kGroups; ++j) {
+                const uint32_t g = PER == 1 ? 0u : turn * kGroups + j;
+                if (!gm_wait_warp(&c.g_full[st][g], round & 1u, c, P.a.status)) {
+                    ok = false;
+                    break;
                 }
-                const uint32_t acc = c.tmem_base + d * NT;
-if (elect_one()) {
+                tc_fence_after();
+                const uint32_t acc = c.tmem_base + (n * PER + g) % ACCS * NT;
+                // the group's first K step: 8 columns of A and 32 bytes of B each
+                const uint32_t a0 = ta + 8u * kMmas * g;
+                const uint64_t b0 = PER == 1 ? xd0 : (turn ? xd1 : xd0) + 2u * kMmas * j;
+                if (elect_one()) {
 #pragma unroll
-                    for (int k = 0; k < 8 / PER; ++k) {
-                        const int kk = g * (8 / PER) + k;
-                        umma_bf16_ts(acc, ta + 8u * kk, (kk < 4 ? xd0 : xd1) + 2u * (kk & 3), idesc,
+                    for (int k = 0; k < kMmas; ++k)
+                        umma_bf16_ts(acc, a0 + 8u * k,
+                                     PER == 1 && k >= 4 ? xd1 + 2u * (k - 4) : b0 + 2u * k, idesc,
                                      k > 0 ? 1u : 0u);
-                    }
-                    if (!A::by_slice && g == PER - 1) mbar_arrive(&c.order[turn ^ 1u]);
                     umma_commit(&c.done[st][g]);
+                    if (j == kGroups - 1) umma_commit(&c.s_free[st]);
                 }
                 __syncwarp();
                 issued = true;
@@ -476,8 +482,8 @@ if (elect_one()) {
         }
         count = end;
     }
-    if (issued) {  // every MMA has finished before the block ends (issued by this lane: elect.sync
-                   // picks the same one each time)
+    if (issued) {  // every MMA has finished before the block ends (elect.sync picks one lane
+                   // throughout, so the commit covers all of the warp's)
         if (elect_one()) umma_commit(&c.drain[turn]);
         mbar_wait(&c.drain[turn], 0, nullptr);
     }
@@ -506,25 +512,33 @@ __device__ __forceinline__ void tmem_ld_cols(uint32_t a, uint32_t (&v)[32]) {
         : "r"(a));
     asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 }
+// (two loads: one of 64 registers does not fit those of a thread at launch)
 __device__ __forceinline__ void tmem_ld_cols(uint32_t a, uint32_t (&v)[64]) {
     asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x64.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,"
-        "%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32,%33,%34,%35,%36,"
-        "%37,%38,%39,%40,%41,%42,%43,%44,%45,%46,%47,%48,%49,%50,%51,%52,%53,%54,%55,%56,%57,%58,"
-        "%59,%60,%61,%62,%63}, [%64];"
-        : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]),
-          "=r"(v[7]), "=r"(v[8]), "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]),
-          "=r"(v[14]), "=r"(v[15]), "=r"(v[16]), "=r"(v[17]), "=r"(v[18]), "=r"(v[19]),
-          "=r"(v[20]), "=r"(v[21]), "=r"(v[22]), "=r"(v[23]), "=r"(v[24]), "=r"(v[25]),
-          "=r"(v[26]), "=r"(v[27]), "=r"(v[28]), "=r"(v[29]), "=r"(v[30]), "=r"(v[31]),
-          "=r"(v[32]), "=r"(v[33]), "=r"(v[34]), "=r"(v[35]), "=r"(v[36]), "=r"(v[37]),
-          "=r"(v[38]), "=r"(v[39]), "=r"(v[40]), "=r"(v[41]), "=r"(v[42]), "=r"(v[43]),
-          "=r"(v[44]), "=r"(v[45]), "=r"(v[46]), "=r"(v[47]), "=r"(v[48]), "=r"(v[49]),
-          "=r"(v[50]), "=r"(v[51]), "=r"(v[52]), "=r"(v[53]), "=r"(v[54]), "=r"(v[55]),
-          "=r"(v[56]), "=r"(v[57]), "=r"(v[58]), "=r"(v[59]), "=r"(v[60]), "=r"(v[61]),
-          "=r"(v[62]), "=r"(v[63])
-        : "r"(a));
-    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {"
+        "%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,"
+        "%25,%26,%27,%28,%29,%30,%31"
+        "}, [%64];\n\t"
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {"
+        "%32,%33,%34,%35,%36,%37,%38,%39,%40,%41,%42,%43,%44,%45,%46,%47,%48,%49,%50,%51,%52,%53,"
+        "%54,%55,%56,%57,%58,%59,%60,%61,%62,%63"
+        "}, [%65];\n\t"
+        "tcgen05.wait::ld.sync.aligned;"
+        : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]),
+          "=r"(v[5]), "=r"(v[6]), "=r"(v[7]), "=r"(v[8]), "=r"(v[9]),
+          "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]),
+          "=r"(v[15]), "=r"(v[16]), "=r"(v[17]), "=r"(v[18]), "=r"(v[19]),
+          "=r"(v[20]), "=r"(v[21]), "=r"(v[22]), "=r"(v[23]), "=r"(v[24]),
+          "=r"(v[25]), "=r"(v[26]), "=r"(v[27]), "=r"(v[28]), "=r"(v[29]),
+          "=r"(v[30]), "=r"(v[31]), "=r"(v[32]), "=r"(v[33]), "=r"(v[34]),
+          "=r"(v[35]), "=r"(v[36]), "=r"(v[37]), "=r"(v[38]), "=r"(v[39]),
+          "=r"(v[40]), "=r"(v[41]), "=r"(v[42]), "=r"(v[43]), "=r"(v[44]),
+          "=r"(v[45]), "=r"(v[46]), "=r"(v[47]), "=r"(v[48]), "=r"(v[49]),
+          "=r"(v[50]), "=r"(v[51]), "=r"(v[52]), "=r"(v[53]), "=r"(v[54]),
+          "=r"(v[55]), "=r"(v[56]), "=r"(v[57]), "=r"(v[58]), "=r"(v[59]),
+          "=r"(v[60]), "=r"(v[61]), "=r"(v[62]), "=r"(v[63])
+        : "r"(a), "r"(a + 32u)
+        : "memory");
 }
 
 // Two FP32 FMAs in one instruction, each rounded to nearest.
@@ -543,7 +557,7 @@ template <int NT, bool HALF, int PER>
 __device__ void gm_scale(const GmParams& P, const GmSmem& S, int wi, int lane) {
     GmCtl& c = *S.ctl;
     const Q4Layout& L = P.L;
-    using A = Acc<NT, PER>;
+    constexpr uint32_t ACCS = accs<NT, PER>();
     constexpr int HN = NT / 2;  // columns of this warp
     const uint32_t q = uint32_t(wi) & 3u, half = uint32_t(wi) >> 2;
     const uint32_t r = 32u * q + uint32_t(lane);
@@ -552,8 +566,8 @@ __device__ void gm_scale(const GmParams& P, const GmSmem& S, int wi, int lane) {
     const uint32_t t_lane = c.tmem_base + ((32u * q) << 16) + half * HN;
     uint32_t s0, s1, e = 0, count = 0;
     my_slices(P, s0, s1);
-    if (A::by_slice && lane == 0)  // the first slices' accumulators are free
-        for (uint32_t k = 0; k < A::slices; ++k) mbar_arrive(&c.s_full[k]);
+    if (lane == 0)  // the first groups' accumulators are free
+        for (uint32_t k = 0; k < ACCS; ++k) mbar_arrive(&c.g_full[k / PER][k % PER]);
     for (uint32_t u = blockIdx.x / P.split;; u += gridDim.x / P.split) {
         const GmUnit t = unit_at<NT>(P, S, u, e);
         if (!t.valid) return;
@@ -564,40 +578,30 @@ __device__ void gm_scale(const GmParams& P, const GmSmem& S, int wi, int lane) {
         const uint32_t live = t.ntok > half * HN ? t.ntok - half * HN : 0u;  // columns in use
         for (const uint32_t end = count + (s1 - s0); count < end; ++count) {
             const uint32_t st = count % kSRing, round = count / kSRing, ws = count % kWRing;
-            if (!gm_wait_warp(&c.w_full[ws], (count / kWRing) & 1u, c, P.a.status)) return;
-            float sc[PER];
 #pragma unroll
             for (int g = 0; g < PER; ++g) {
-                uint16_t b;
-                asm volatile("ld.shared.u16 %0, [%1];"
-                             : "=h"(b)
-                             : "r"(scale_at + ws * kWStage + 32u * g));
-                sc[g] = q4_scale(b, half_scales);
-            }
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&c.w_empty[ws]);
-#pragma unroll
-            for (int g = 0; g < PER; ++g) {
-                const uint32_t gi = count * PER + g;
-                const uint32_t d = A::by_slice ? (count % A::slices) * PER + g : gi % A::ring;
+                const uint32_t gi = count * PER + g, next = gi + ACCS;
                 if (!gm_wait_warp(&c.done[st][g], round & 1u, c, P.a.status)) return;
                 tc_fence_after();
+                // The group's MMAs are done, so its records have long landed
+                // (the unpacking warps waited for them) and stay until this
+                // warp's word on w_empty: no wait of its own.
+                uint16_t bits;
+                asm volatile("ld.shared.u16 %0, [%1];"
+                             : "=h"(bits)
+                             : "r"(scale_at + ws * kWStage + 32u * g));
+                uint32_t v[HN];
+                if (live > 0) tmem_ld_cols(t_lane + gi % ACCS * NT, v);
+                tc_fence_before();
+                const float sc = q4_scale(bits, half_scales);
+                __syncwarp();
+                if (lane == 0) {
+                    mbar_arrive(&c.g_full[next / PER % kSRing][next % PER]);
+                    if (g == PER - 1) mbar_arrive(&c.w_empty[ws]);
+                }
                 if (live > 0) {
-                    uint32_t v[HN];
-                    tmem_ld_cols(t_lane + d * NT, v);
-                    if (!A::by_slice || g == PER - 1) {
-                        tc_fence_before();
-                        __syncwarp();
-                        if (lane == 0)
-                            mbar_arrive(A::by_slice ? &c.s_full[(count + A::slices) % kSRing]
-                                                    : &c.acc_empty[d]);
-                    }
 #pragma unroll
-                    for (int k = 0; k < HN / 2; ++k) fma2(sum[k], sc[g], v[2 * k], v[2 * k + 1]);
-                } else if (!A::by_slice || g == PER - 1) {
-                    if (lane == 0)
-                        mbar_arrive(A::by_slice ? &c.s_full[(count + A::slices) % kSRing]
-                                                : &c.acc_empty[d]);
+                    for (int k = 0; k < HN / 2; ++k) fma2(sum[k], sc, v[2 * k], v[2 * k + 1]);
                 }
             }
         }
@@ -642,16 +646,16 @@ __global__ void __launch_bounds__(kQ4GemmThreads, 1)
             mbar_init(&c.w_full[s], 1);
             mbar_init(&c.w_empty[s], 4 + kSclWarps);
         }
-        const uint32_t free_acc = Acc<NT, PER>::by_slice ? kSclWarps : 0;
         for (uint32_t s = 0; s < kSRing; ++s) {
-            mbar_init(&c.s_full[s], 4 + (P.x_bytes == 16 ? 1 : 32) + free_acc);
-            for (int g = 0; g < PER; ++g) mbar_init(&c.done[s][g], 1);
+            for (int g = 0; g < PER; ++g) {
+                const bool first = g == 0 || (PER > 1 && g == PER / 2);  // of a panel
+                mbar_init(&c.g_full[s][g],
+                          4 + kSclWarps + (!first ? 0 : P.x_bytes == 16 ? 1 : 32));
+                mbar_init(&c.done[s][g], 1);
+            }
+            mbar_init(&c.s_free[s], PER == 1 ? 1 : kMWarps);
         }
-        for (uint32_t s = 0; s < 4; ++s) mbar_init(&c.acc_empty[s], kSclWarps);
-        for (int s = 0; s < kMWarps; ++s) {
-            mbar_init(&c.drain[s], 1);
-            mbar_init(&c.order[s], 1);
-        }
+        for (int s = 0; s < kMWarps; ++s) mbar_init(&c.drain[s], 1);
         c.abort = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
@@ -710,17 +714,17 @@ __global__ void __launch_bounds__(kQ4GemmThreads, 1)
             gm_load_x_any<NT, PER, 2>(P, S, lane);
         }
         __syncthreads();  // (no warp spins for the registers that the scaling warps hold)
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 96;");
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsLaunch));
     } else if (warp < kSclWarp0) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsUnpack));
         gm_unpack<NT, HALF, PER>(P, S, warp - kUnpWarp0, lane);
         __syncthreads();
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 96;");
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsLaunch));
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsScale));
         gm_scale<NT, HALF, PER>(P, S, warp - kSclWarp0, lane);
         __syncthreads();
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 96;");
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsLaunch));
     }
     __syncwarp();
     if (P.split > 1) {
