@@ -162,9 +162,27 @@ __device__ __forceinline__ bool gm_wait_more(unsigned long long* bar, uint32_t p
                                              int32_t* status) {
     uint64_t t0 = 0;
     for (;;) {
-#pragma unroll 1
-        for (int k = 0; k < 256; ++k)
-            if (gm_poll(bar, parity)) return true;
+        // polls are the only instructions of this loop: what a waiting warp
+        // issues, the others of its scheduler do not
+        uint32_t done;
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t.reg .u32 k;\n\t"
+            "mov.u32 k, 64;\n\t"
+            "MORE:\n\t"
+            "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t@p bra DONE;\n\t"
+            "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t@p bra DONE;\n\t"
+            "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t@p bra DONE;\n\t"
+            "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t@p bra DONE;\n\t"
+            "sub.u32 k, k, 1;\n\t"
+            "setp.ne.u32 p, k, 0;\n\t"
+            "@p bra MORE;\n\t"
+            "setp.ne.u32 p, k, k;\n\t"
+            "DONE:\n\t"
+            "selp.u32 %0, 1, 0, p;\n\t}"
+            : "=r"(done)
+            : "r"(smem_addr(bar)), "r"(parity)
+            : "memory");
+        if (done) return true;
         const uint64_t t = global_timer_ns();
         if (t0 == 0) t0 = t;
         if (*const_cast<volatile int*>(&c.abort)) return false;
@@ -541,16 +559,22 @@ __device__ __forceinline__ void tmem_ld_cols(uint32_t a, uint32_t (&v)[64]) {
         : "memory");
 }
 
-// Two FP32 FMAs in one instruction, each rounded to nearest.
-__device__ __forceinline__ void fma2(float2& acc, float s, uint32_t v0, uint32_t v1) {
-    asm("{\n\t.reg .b64 a, b, d;\n\t"
-        "mov.b64 a, {%2, %2};\n\t"
-        "mov.b64 b, {%3, %4};\n\t"
-        "mov.b64 d, {%0, %1};\n\t"
-        "fma.rn.f32x2 d, a, b, d;\n\t"
-        "mov.b64 {%0, %1}, d;\n\t}"
-        : "+f"(acc.x), "+f"(acc.y)
-        : "f"(s), "r"(v0), "r"(v1));
+// Two FP32 FMAs in one instruction, each rounded to nearest; the sums stay
+// register pairs.
+__device__ __forceinline__ void fma2(uint64_t& acc, uint64_t s2, uint32_t v0, uint32_t v1) {
+    asm("{\n\t.reg .b64 b;\n\t"
+        "mov.b64 b, {%2, %3};\n\t"
+        "fma.rn.f32x2 %0, %1, b, %0;\n\t}"
+        : "+l"(acc)
+        : "l"(s2), "r"(v0), "r"(v1));
+}
+__device__ __forceinline__ uint64_t pair2(float s) {
+    uint64_t d;
+    asm("mov.b64 %0, {%1, %1};" : "=l"(d) : "f"(s));
+    return d;
+}
+__device__ __forceinline__ float half2f(uint64_t v, int hi) {
+    return __uint_as_float(uint32_t(hi ? v >> 32 : v));
 }
 
 template <int NT, bool HALF, int PER>
@@ -572,9 +596,9 @@ __device__ void gm_scale(const GmParams& P, const GmSmem& S, int wi, int lane) {
         const GmUnit t = unit_at<NT>(P, S, u, e);
         if (!t.valid) return;
         e = t.e;
-        float2 sum[HN / 2];
+        uint64_t sum[HN / 2];
 #pragma unroll
-        for (int k = 0; k < HN / 2; ++k) sum[k] = make_float2(0.f, 0.f);
+        for (int k = 0; k < HN / 2; ++k) sum[k] = 0;  // two FP32 zeros
         const uint32_t live = t.ntok > half * HN ? t.ntok - half * HN : 0u;  // columns in use
         for (const uint32_t end = count + (s1 - s0); count < end; ++count) {
             const uint32_t st = count % kSRing, round = count / kSRing, ws = count % kWRing;
@@ -593,7 +617,7 @@ __device__ void gm_scale(const GmParams& P, const GmSmem& S, int wi, int lane) {
                 uint32_t v[HN];
                 if (live > 0) tmem_ld_cols(t_lane + gi % ACCS * NT, v);
                 tc_fence_before();
-                const float sc = q4_scale(bits, half_scales);
+                const uint64_t sc = pair2(q4_scale(bits, half_scales));
                 __syncwarp();
                 if (lane == 0) {
                     mbar_arrive(&c.g_full[next / PER % kSRing][next % PER]);
@@ -612,13 +636,13 @@ __device__ void gm_scale(const GmParams& P, const GmSmem& S, int wi, int lane) {
                 for (int k = 0; k < HN; ++k)
                     if (uint32_t(k) < live)
                         store_y<HALF>(P, uint64_t(t.tok0) + half * HN + k, row,
-                                      k & 1 ? sum[k / 2].y : sum[k / 2].x);
+                                      half2f(sum[k / 2], k & 1));
             }
         } else {  // the block's only unit: every copy into the ring has been used
             float* red = reinterpret_cast<float*>(S.x);
 #pragma unroll
             for (int k = 0; k < HN; ++k)
-                red[(half * HN + k) * kRowsTile + r] = k & 1 ? sum[k / 2].y : sum[k / 2].x;
+                red[(half * HN + k) * kRowsTile + r] = half2f(sum[k / 2], k & 1);
         }
     }
 }
