@@ -485,8 +485,9 @@ int wc_decompress_tans_batch(const wc_batch_item *h_items, uint32_t count, int32
  *                    or, with WC_Q4_ZEROS, lo = min(w, 0), hi = max(w, 0),
  *                      s = round16((hi - lo) / 15), z = clamp(rint(-lo/s), 0, 15),
  *                      q = clamp(rint(w/s) + z, 0, 15)
- *                    s = 0: every code stands for zero. A NaN in a group makes
- *                    its scale NaN; an infinity makes it infinite.
+ *                    s = 0: every code stands for zero. A NaN in a group, or
+ *                    infinities of both signs, makes its scale NaN; other
+ *                    infinities make it infinite.
  *  wc_q4_pack        the stream of given codes (u8, rows x cols, low 4 bits
  *                    used), scales (u16, rows x groups) and zero points (u8,
  *                    rows x groups; with WC_Q4_ZEROS, else NULL), all dense:

@@ -15,8 +15,9 @@ namespace cg = cooperative_groups;
 // ---------------------------------------------------------------------------
 // Counting sort of the slots by expert, stable: row = first row of the expert +
 // earlier slots of the same expert. One cluster of up to 8 blocks: each warp
-// owns consecutive slots and counts them in its own histogram (lanes of one
-// expert matched, so no atomics); the histograms are scanned over the block's
+// owns consecutive slots and counts them in its own histogram (the lanes of one
+// expert found by a ballot per bit of the id, so no atomics); the histograms are
+// scanned over the block's
 // warps, the cluster's blocks (through distributed shared memory) and the
 // experts; then each warp walks its slots again. No workspace and one launch;
 // the ids are read twice, the second time from L2. A few hundred thousand slots
@@ -25,6 +26,18 @@ namespace cg = cooperative_groups;
 constexpr int kSortThreads = 1024;
 constexpr int kSortWarps = kSortThreads / 32;
 constexpr uint32_t kMaxExperts = 1024;
+
+// Lanes of the warp whose id equals this lane's (ids < 2^bits).
+__device__ __forceinline__ uint32_t same_id(uint32_t id, int bits) {
+    uint32_t m = 0xFFFFFFFFu;
+    for (int b = 0; b < bits; ++b) {
+        const uint32_t set = __ballot_sync(0xFFFFFFFFu, (id >> b) & 1u);
+        m &= (id >> b) & 1u ? set : ~set;
+    }
+    return m;
+}
+
+constexpr int kSortBatch = 8;  // ids of a lane loaded ahead of the dependent counting
 
 __global__ void __launch_bounds__(kSortThreads)
     moe_sort_kernel(const int32_t* __restrict__ ids, uint32_t slots, uint32_t experts,
@@ -46,11 +59,21 @@ __global__ void __launch_bounds__(kSortThreads)
     uint32_t* mine = hist + warp * experts;
     for (uint32_t k = tid; k < kSortWarps * experts; k += kSortThreads) hist[k] = 0;
     __syncthreads();
-    for (uint32_t s = begin; s < end; s += 32) {
-        const uint32_t id = s + lane < end ? uint32_t(ids[s + lane]) : experts;
-        const uint32_t same = __match_any_sync(0xFFFFFFFFu, id);
-        if (id < experts && (same & ((1u << lane) - 1u)) == 0) mine[id] += __popc(same);
-        __syncwarp();
+    const int bits = 32 - __clz(int(experts));  // ids and the dropped ones' `experts`
+    const uint32_t below = (1u << lane) - 1u;
+    for (uint32_t s0 = begin; s0 < end; s0 += 32 * kSortBatch) {
+        uint32_t id[kSortBatch];
+#pragma unroll
+        for (int k = 0; k < kSortBatch; ++k)
+            id[k] = s0 + 32 * k + lane < end ? min(uint32_t(ids[s0 + 32 * k + lane]), experts)
+                                             : experts;
+#pragma unroll
+        for (int k = 0; k < kSortBatch; ++k) {
+            if (s0 + 32 * k >= end) break;
+            const uint32_t same = same_id(id[k], bits);
+            if (id[k] < experts && (same & below) == 0) mine[id[k]] += __popc(same);
+            __syncwarp();
+        }
     }
     __syncthreads();
     for (uint32_t e = tid; e < experts; e += kSortThreads) {
@@ -92,20 +115,30 @@ __global__ void __launch_bounds__(kSortThreads)
     uint32_t rows = 0;
     for (int w = 0; w < kSortWarps; ++w) rows += warp_sum[w];
     __syncthreads();
-    for (uint32_t s = begin; s < end; s += 32) {
-        const bool live = s + lane < end;
-        const uint32_t id = live ? uint32_t(ids[s + lane]) : experts;
-        const uint32_t same = __match_any_sync(0xFFFFFFFFu, id);
-        int32_t pos = -1;
-        if (id < experts) pos = int32_t(base[id] + mine[id] + __popc(same & ((1u << lane) - 1u)));
-        __syncwarp();
-        if (id < experts && (same & ((1u << lane) - 1u)) == 0) mine[id] += __popc(same);
-        __syncwarp();
-        if (live) {
-            inverse[s + lane] = pos;
-            if (order != nullptr && pos >= 0) order[pos] = int32_t(s + lane);
+    for (uint32_t s0 = begin; s0 < end; s0 += 32 * kSortBatch) {
+        uint32_t id[kSortBatch];
+#pragma unroll
+        for (int k = 0; k < kSortBatch; ++k)
+            id[k] = s0 + 32 * k + lane < end ? min(uint32_t(ids[s0 + 32 * k + lane]), experts)
+                                             : experts;
+#pragma unroll
+        for (int k = 0; k < kSortBatch; ++k) {
+            const uint32_t s = s0 + 32 * k + lane;
+            if (s0 + 32 * k >= end) break;
+            const uint32_t same = same_id(id[k], bits);
+            int32_t pos = -1;
+            if (id[k] < experts) pos = int32_t(base[id[k]] + mine[id[k]] + __popc(same & below));
+            __syncwarp();
+            if (id[k] < experts && (same & below) == 0) mine[id[k]] += __popc(same);
+            __syncwarp();
+            if (s < end) {
+                inverse[s] = pos;
+                if (order != nullptr) {
+                    if (pos >= 0) order[pos] = int32_t(s);
+                    if (s >= rows) order[s] = -1;
+                }
+            }
         }
-        if (order != nullptr && live && s + lane >= rows) order[s + lane] = -1;
     }
 }
 
@@ -152,11 +185,22 @@ __device__ __forceinline__ V pack(const float (&f)[sizeof(V) / sizeof(T)]) {
     return v;
 }
 
+// A read of data used once: not kept in L1.
+template <typename V>
+__device__ __forceinline__ V ldg_stream(const V* p) {
+    return __ldcs(p);
+}
+template <>
+__device__ __forceinline__ uint16_t ldg_stream<uint16_t>(const uint16_t* p) {
+    return __ldcs(reinterpret_cast<const unsigned short*>(p));
+}
+
 struct RowParams {
     uint64_t tokens, rows;
     uint32_t top;
     uint32_t nvec;      // vectors of a row
     uint32_t segs;      // segments of a row
+    uint32_t team;      // backward: threads of a token
     const int32_t* inverse;
 };
 
@@ -184,7 +228,12 @@ __global__ void __launch_bounds__(kRowThreads)
     }
 }
 
-template <typename T, typename V>
+// Slots are taken kAhead at a time, their rows' vectors all on their way before
+// the first is used (a slot without a row loads nothing and adds nothing): one
+// slot after the other left the memory waiting for indices (186 -> MEASURED).
+constexpr int kAhead = 4;
+
+template <typename T, typename V, int UNROLL>
 __global__ void __launch_bounds__(kRowThreads)
     moe_combine_kernel(RowParams P, const uint8_t* __restrict__ y, uint64_t ldy,
                        const float* __restrict__ weights, uint8_t* __restrict__ out, uint64_t ldo) {
@@ -193,32 +242,49 @@ __global__ void __launch_bounds__(kRowThreads)
     const uint64_t unit = (uint64_t(blockIdx.x) * kRowThreads + threadIdx.x) >> 5;
     const uint64_t tok = unit / P.segs;
     if (tok >= P.tokens) return;
-    const uint32_t v0 = uint32_t(unit % P.segs) * (32 * kUnroll) + lane;
-    float acc[kUnroll][N] = {};
-    for (uint32_t j = 0; j < P.top; ++j) {
-        const int32_t p = P.inverse[tok * P.top + j];
-        if (p < 0 || uint64_t(p) >= P.rows) continue;
-        const float w = weights != nullptr ? weights[tok * P.top + j] : 1.f;
-        const V* src = reinterpret_cast<const V*>(y + uint64_t(p) * ldy);
+    const uint32_t v0 = uint32_t(unit % P.segs) * (32 * UNROLL) + lane;
+    float acc[UNROLL][N] = {};
+    for (uint32_t j0 = 0; j0 < P.top; j0 += kAhead) {
+        int32_t p[kAhead];
+        float w[kAhead];
 #pragma unroll
-        for (int k = 0; k < kUnroll; ++k)
-            if (v0 + 32 * k < P.nvec) {
-                float f[N];
-                unpack<T, V>(src[v0 + 32 * k], f);
+        for (int j = 0; j < kAhead; ++j) {
+            p[j] = j0 + j < P.top ? P.inverse[tok * P.top + j0 + j] : -1;
+            if (p[j] >= 0 && uint64_t(p[j]) >= P.rows) p[j] = -1;
+            w[j] = weights != nullptr && p[j] >= 0 ? weights[tok * P.top + j0 + j] : 1.f;
+        }
+        V v[kAhead][UNROLL];
 #pragma unroll
-                for (int i = 0; i < N; ++i) acc[k][i] = fmaf(w, f[i], acc[k][i]);
-            }
+        for (int j = 0; j < kAhead; ++j)
+#pragma unroll
+            for (int k = 0; k < UNROLL; ++k)
+                if (p[j] >= 0 && v0 + 32 * k < P.nvec)
+                    v[j][k] = ldg_stream(reinterpret_cast<const V*>(y + uint64_t(p[j]) * ldy) + v0 + 32 * k);
+#pragma unroll
+        for (int j = 0; j < kAhead; ++j) {
+            if (p[j] < 0) continue;
+#pragma unroll
+            for (int k = 0; k < UNROLL; ++k)
+                if (v0 + 32 * k < P.nvec) {
+                    float f[N];
+                    unpack<T, V>(v[j][k], f);
+#pragma unroll
+                    for (int i = 0; i < N; ++i) acc[k][i] = fmaf(w[j], f[i], acc[k][i]);
+                }
+        }
     }
     V* dst = reinterpret_cast<V*>(out + tok * ldo);
 #pragma unroll
-    for (int k = 0; k < kUnroll; ++k)
+    for (int k = 0; k < UNROLL; ++k)
         if (v0 + 32 * k < P.nvec) dst[v0 + 32 * k] = pack<T, V>(acc[k]);
 }
 
-// dy[p] = w * dout[token] and dw = <dout[token], y[p]> of each slot: a block
-// owns a token, so that dout is read once and each product's sum stays in
-// registers until one reduction in a fixed order.
-constexpr int kBwSlots = 8;  // slots in flight; more are taken in turns
+// dy[p] = w * dout[token] and dw = <dout[token], y[p]> of each slot: P.team
+// threads (32 to 256) own a token, so that dout is read once and each product's
+// sum stays in registers until one reduction in a fixed order. Slots are taken
+// kBwSlots at a time, with two vectors of each on their way.
+constexpr int kBwSlots = 4;
+constexpr int kBwUnroll = 2;
 
 template <typename T, typename V>
 __global__ void __launch_bounds__(kRowThreads)
@@ -228,8 +294,10 @@ __global__ void __launch_bounds__(kRowThreads)
                                 uint64_t lddy, float* __restrict__ dweights) {
     constexpr int N = sizeof(V) / sizeof(T);
     __shared__ float red[kBwSlots][kRowThreads / 32];
-    const uint32_t tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const uint64_t tok = blockIdx.x;
+    const uint32_t lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const uint32_t tid = threadIdx.x % P.team;
+    const uint64_t tok = uint64_t(blockIdx.x) * (kRowThreads / P.team) + threadIdx.x / P.team;
+    const bool live = tok < P.tokens;  // (every thread reaches the barriers)
     const V* d = reinterpret_cast<const V*>(dout + tok * ldd);
     for (uint32_t j0 = 0; j0 < P.top; j0 += kBwSlots) {
         int32_t p[kBwSlots];
@@ -239,26 +307,44 @@ __global__ void __launch_bounds__(kRowThreads)
             dot[j] = 0.f;
             w[j] = 1.f;
             p[j] = -1;
-            if (j0 + j < P.top) {
+            if (live && j0 + j < P.top) {
                 p[j] = P.inverse[tok * P.top + j0 + j];
                 if (p[j] >= 0 && uint64_t(p[j]) >= P.rows) p[j] = -1;
                 if (weights != nullptr) w[j] = weights[tok * P.top + j0 + j];
             }
         }
-        for (uint32_t v = tid; v < P.nvec; v += blockDim.x) {
-            float df[N];
-            unpack<T, V>(d[v], df);
+        if (live) {
+            for (uint32_t v0 = tid; v0 < P.nvec; v0 += kBwUnroll * P.team) {
+                V dv[kBwUnroll], yv[kBwSlots][kBwUnroll];
 #pragma unroll
-            for (int j = 0; j < kBwSlots; ++j) {
-                if (p[j] < 0) continue;
-                float f[N];
-                unpack<T, V>(reinterpret_cast<const V*>(y + uint64_t(p[j]) * ldy)[v], f);
+                for (int k = 0; k < kBwUnroll; ++k) {
+                    const uint32_t v = v0 + k * P.team;
+                    if (v >= P.nvec) continue;
+                    dv[k] = d[v];
 #pragma unroll
-                for (int i = 0; i < N; ++i) {
-                    dot[j] = fmaf(df[i], f[i], dot[j]);
-                    f[i] = w[j] * df[i];
+                    for (int j = 0; j < kBwSlots; ++j)
+                        if (p[j] >= 0)
+                            yv[j][k] = ldg_stream(reinterpret_cast<const V*>(y + uint64_t(p[j]) * ldy) + v);
                 }
-                reinterpret_cast<V*>(dy + uint64_t(p[j]) * lddy)[v] = pack<T, V>(f);
+#pragma unroll
+                for (int k = 0; k < kBwUnroll; ++k) {
+                    const uint32_t v = v0 + k * P.team;
+                    if (v >= P.nvec) continue;
+                    float df[N];
+                    unpack<T, V>(dv[k], df);
+#pragma unroll
+                    for (int j = 0; j < kBwSlots; ++j) {
+                        if (p[j] < 0) continue;
+                        float f[N];
+                        unpack<T, V>(yv[j][k], f);
+#pragma unroll
+                        for (int i = 0; i < N; ++i) {
+                            dot[j] = fmaf(df[i], f[i], dot[j]);
+                            f[i] = w[j] * df[i];
+                        }
+                        reinterpret_cast<V*>(dy + uint64_t(p[j]) * lddy)[v] = pack<T, V>(f);
+                    }
+                }
             }
         }
         if (dweights != nullptr) {
@@ -269,9 +355,10 @@ __global__ void __launch_bounds__(kRowThreads)
                 if (lane == 0) red[j][warp] = dot[j];
             }
             __syncthreads();
-            if (tid < kBwSlots && j0 + tid < P.top) {
+            if (live && tid < kBwSlots && j0 + tid < P.top) {
+                const uint32_t w0 = threadIdx.x / P.team * (P.team / 32);
                 float sum = 0.f;
-                for (uint32_t k = 0; k < blockDim.x / 32; ++k) sum += red[tid][k];
+                for (uint32_t k = 0; k < P.team / 32; ++k) sum += red[tid][w0 + k];
                 dweights[tok * P.top + j0 + tid] = sum;
             }
             __syncthreads();
@@ -310,13 +397,14 @@ cudaError_t by_type(uint32_t dtype, uint32_t v, F f) {
     return f(__nv_bfloat16(), uint16_t());
 }
 
-RowParams row_params(const MoeArgs& a, uint32_t v) {
+RowParams row_params(const MoeArgs& a, uint32_t v, int unroll = kUnroll) {
     RowParams P;
     P.tokens = a.tokens;
     P.rows = a.rows;
     P.top = a.top;
     P.nvec = uint32_t(a.cols * elem_size(a.dtype) / v);
-    P.segs = (P.nvec + 32 * kUnroll - 1) / (32 * kUnroll);
+    P.segs = (P.nvec + 32 * unroll - 1) / (32 * unroll);
+    P.team = 32;
     P.inverse = a.inverse;
     return P;
 }
@@ -387,14 +475,19 @@ cudaError_t launch_moe_combine(const MoeArgs& a, const void* y, uint64_t ldy, co
     const uint32_t v = vec_bytes(reinterpret_cast<uintptr_t>(y) | (ldy * es) |
                                      reinterpret_cast<uintptr_t>(out) | (ldo * es) | (a.cols * es),
                                  es);
-    const RowParams P = row_params(a, v);
+    // Two vectors a lane where a row is long enough to fill the machine so, one
+    // where there are few rows.
+    const uint64_t vectors = a.tokens * (a.cols * es / v);
+    const int unroll = vectors >= (1u << 19) ? 2 : 1;
+    const RowParams P = row_params(a, v, unroll);
     const uint64_t blocks = (a.tokens * P.segs * 32 + kRowThreads - 1) / kRowThreads;
     if (blocks > 0x7FFFFFFFull) return too_large();
     return by_type(a.dtype, v, [&](auto t, auto vec) {
-        moe_combine_kernel<decltype(t), decltype(vec)>
-            <<<uint32_t(blocks), kRowThreads, 0, stream>>>(P, static_cast<const uint8_t*>(y),
-                                                           ldy * es, weights,
-                                                           static_cast<uint8_t*>(out), ldo * es);
+        const auto kernel = unroll == 2 ? moe_combine_kernel<decltype(t), decltype(vec), 2>
+                                        : moe_combine_kernel<decltype(t), decltype(vec), 1>;
+        kernel<<<uint32_t(blocks), kRowThreads, 0, stream>>>(P, static_cast<const uint8_t*>(y),
+                                                             ldy * es, weights,
+                                                             static_cast<uint8_t*>(out), ldo * es);
         return cudaGetLastError();
     });
 }
@@ -409,13 +502,14 @@ cudaError_t launch_moe_combine_backward(const MoeArgs& a, const void* dout, uint
                                      reinterpret_cast<uintptr_t>(y) | (ldy * es) |
                                      reinterpret_cast<uintptr_t>(dy) | (lddy * es) | (a.cols * es),
                                  es);
-    const RowParams P = row_params(a, v);
-    if (a.tokens > 0x7FFFFFFFull) return too_large();
-    uint32_t threads = 32;
-    while (threads < uint32_t(kRowThreads) && threads < P.nvec) threads *= 2;
+    RowParams P = row_params(a, v);
+    while (P.team < uint32_t(kRowThreads) && P.team * kBwUnroll < P.nvec) P.team *= 2;
+    const uint64_t per = kRowThreads / P.team;
+    const uint64_t blocks = (a.tokens + per - 1) / per;
+    if (blocks > 0x7FFFFFFFull) return too_large();
     return by_type(a.dtype, v, [&](auto t, auto vec) {
         moe_combine_backward_kernel<decltype(t), decltype(vec)>
-            <<<uint32_t(a.tokens), threads, 0, stream>>>(
+            <<<uint32_t(blocks), kRowThreads, 0, stream>>>(
                 P, static_cast<const uint8_t*>(dout), ldd * es, static_cast<const uint8_t*>(y),
                 ldy * es, weights, static_cast<uint8_t*>(dy), lddy * es, dweights);
         return cudaGetLastError();

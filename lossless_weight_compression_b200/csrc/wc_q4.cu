@@ -26,15 +26,70 @@ __device__ __forceinline__ uint16_t from_float(float v) {
 }
 
 // Eight consecutive 16-bit values of a row from column c, zeros past the end.
+// `vec`: bytes that divide the address of every row (2 to 16).
 __device__ __forceinline__ uint4 load8(const uint16_t* row, uint32_t c, uint32_t cols, bool live,
-                                       bool vec) {
+                                       uint32_t vec) {
     if (!live || c >= cols) return make_uint4(0, 0, 0, 0);
-    if (vec && c + 8 <= cols) return ld_stream_v4(row + c);
+    if (vec >= 4 && c + 8 <= cols) {
+        if (vec == 16) return ld_stream_v4(row + c);
+        if (vec == 8) {
+            const uint2 a = __ldcs(reinterpret_cast<const uint2*>(row + c));
+            const uint2 b = __ldcs(reinterpret_cast<const uint2*>(row + c + 4));
+            return make_uint4(a.x, a.y, b.x, b.y);
+        }
+        const uint32_t* p = reinterpret_cast<const uint32_t*>(row + c);
+        return make_uint4(__ldcs(p), __ldcs(p + 1), __ldcs(p + 2), __ldcs(p + 3));
+    }
     uint32_t v[4] = {0, 0, 0, 0};
 #pragma unroll
     for (uint32_t k = 0; k < 8; ++k)
         if (c + k < cols) v[k >> 1] |= uint32_t(row[c + k]) << (16 * (k & 1));
     return make_uint4(v[0], v[1], v[2], v[3]);
+}
+
+// Eight 16-bit values to a row from column c, up to the last column.
+__device__ __forceinline__ void store8(uint16_t* row, uint32_t c, uint32_t cols, uint32_t vec,
+                                       uint4 v) {
+    if (vec >= 4 && c + 8 <= cols) {
+        if (vec == 16) {
+            st_stream_v4(row + c, v);
+        } else if (vec == 8) {
+            __stcs(reinterpret_cast<uint2*>(row + c), make_uint2(v.x, v.y));
+            __stcs(reinterpret_cast<uint2*>(row + c + 4), make_uint2(v.z, v.w));
+        } else {
+            uint32_t* p = reinterpret_cast<uint32_t*>(row + c);
+            __stcs(p, v.x);
+            __stcs(p + 1, v.y);
+            __stcs(p + 2, v.z);
+            __stcs(p + 3, v.w);
+        }
+        return;
+    }
+    const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (uint32_t k = 0; k < 8; ++k)
+        if (c + k < cols) row[c + k] = uint16_t(u[k >> 1] >> (16 * (k & 1)));
+}
+
+// Adding and subtracting 1.5 * 2^23 rounds |x| < 2^22 to the nearest integer,
+// ties to even, on the FMA pipe; after the addition the integer sits in the low
+// mantissa bits. (rintf and the conversion to int run at an eighth of its rate:
+// with them and a division a weight the kernel was bound by that unit.)
+constexpr float kRound = 12582912.f;
+
+// rint(w / s) as a float, r = 1 / s rounded. The quotient of the 16-bit values w
+// and s, each an integer of at most 11 bits times a power of two, is either a
+// tie k + 1/2 or at least 2^-13 away from every tie: with s = S 2^b, w = W 2^a,
+// w / s - (2 k + 1) / 2 = (2 W 2^(a-b) - (2 k + 1) S) / (2 S), whose numerator is
+// a multiple of 1/2 (w / s >= 1/4 makes a - b >= -2 for normalised W and S of
+// equal length) and S < 2^11. w * r is off by less than 2^-22 of itself, below
+// 2^-17 for quotients up to 32; so one within 2^-15 of a half-integer is that
+// half-integer, and rounds as the exact quotient does.
+__device__ __forceinline__ float quotient(float w, float r) {
+    const float t = w * r;
+    const float h = fmaf(t, 2.f, kRound) - kRound;  // rint(2 t)
+    const float half = 0.5f * h;
+    return fabsf(t - half) < 3.0517578125e-5f ? half : t;
 }
 
 // The word of eight codes in element order.
@@ -66,12 +121,14 @@ __device__ __forceinline__ void store_header(const Q4Layout& L, uint8_t* out) {
 // exact arithmetic comes within an FP32 rounding of one.
 template <bool HALF>
 __global__ void __launch_bounds__(kQ4Threads)
-    q4_quantize_kernel(const uint16_t* __restrict__ w, uint64_t ld, Q4Layout L, bool vec,
+    q4_quantize_kernel(const uint16_t* __restrict__ w, uint64_t ld, Q4Layout L, uint32_t vec,
                        uint8_t* __restrict__ out) {
     extern __shared__ __align__(16) uint8_t sm[];
     const uint32_t lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const uint32_t b0 = blockIdx.y * 8, s = blockIdx.x;
     const uint32_t h = min(8u, L.blocks16 - b0);
+    const uint32_t lanes = L.group / 8;  // of a group
+    const float steps = L.zeros ? 15.f : 7.f;
     store_header(L, out);
     if (warp < h) {
         uint8_t* rec = sm + warp * L.rec;
@@ -89,28 +146,45 @@ __global__ void __launch_bounds__(kQ4Threads)
             const uint32_t u[4] = {v[k].x, v[k].y, v[k].z, v[k].w};
 #pragma unroll
             for (int e = 0; e < 8; ++e) f[e] = to_float<HALF>(uint16_t(u[e >> 1] >> (16 * (e & 1))));
-            // NaN has to reach the scale, which fminf and fmaxf would drop
-            float lo = 0.f, hi = 0.f, nan = 0.f;
+            // fminf and fmaxf drop a NaN, which has to reach the scale: it enters as
+            // both infinities
+            const float inf = __int_as_float(0x7F800000);
+            float lo = 0.f, hi = 0.f;
+            bool nan = false;
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
                 lo = fminf(lo, f[e]);
                 hi = fmaxf(hi, f[e]);
-                nan += f[e] != f[e] ? 1.f : 0.f;
+                nan |= f[e] != f[e];
             }
-            for (uint32_t o = 1; o < L.group / 8; o *= 2) {
+            if (nan) hi = inf, lo = -inf;
+            for (uint32_t o = 1; o < lanes; o *= 2) {
                 lo = fminf(lo, __shfl_xor_sync(0xFFFFFFFFu, lo, o));
                 hi = fmaxf(hi, __shfl_xor_sync(0xFFFFFFFFu, hi, o));
-                nan += __shfl_xor_sync(0xFFFFFFFFu, nan, o);
             }
-            const float range = L.zeros ? (hi - lo) / 15.f : fmaxf(hi, -lo) / 7.f;
-            const uint16_t sbits = from_float<HALF>(nan > 0.f ? __int_as_float(0x7FC00000) : range);
+            float range = L.zeros ? hi - lo : fmaxf(hi, -lo);
+            if (hi == inf && lo == -inf) range = __int_as_float(0x7FC00000);
+            const uint16_t sbits = from_float<HALF>(range / steps);
             const float sc = to_float<HALF>(sbits);
-            const float d = sc > 0.f ? sc : 1.f;
-            const float z = L.zeros ? fminf(fmaxf(rintf(-lo / d), 0.f), 15.f) : 8.f;
             uint32_t q[8];
+            float z = 8.f;
+            if (sc > 1e-30f && sc < 1e30f) {
+                const float r = 1.f / sc;
+                if (L.zeros) z = fminf((quotient(-lo, r) + kRound) - kRound, 15.f);
+                const float zk = z + kRound;
 #pragma unroll
-            for (int e = 0; e < 8; ++e)
-                q[e] = uint32_t(fminf(fmaxf(rintf(f[e] / d) + z, 0.f), 15.f));
+                for (int e = 0; e < 8; ++e) {
+                    // clamped before the rounding: the bounds are integers
+                    const float t = fminf(fmaxf(quotient(f[e], r), -z), 15.f - z);
+                    q[e] = __float_as_uint((t + kRound) - kRound + zk) & 15u;
+                }
+            } else {  // no scale, one that 1 / s cannot hold, infinity or NaN: the definition's steps
+                const float d = sc > 0.f ? sc : 1.f;
+                if (L.zeros) z = fminf(fmaxf(rintf(-lo / d), 0.f), 15.f);
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    q[e] = uint32_t(fminf(fmaxf(rintf(f[e] / d) + z, 0.f), 15.f));
+            }
             const uint32_t i = c8 >> 2, t = c8 & 3u;
             *reinterpret_cast<uint32_t*>(rec + t * 256 + r * 16 + i * 4) = pack8(q);
             if ((c8 & (L.group / 8 - 1)) == 0) {
@@ -162,7 +236,7 @@ __global__ void __launch_bounds__(kQ4Threads)
 template <int DT>
 __global__ void __launch_bounds__(kQ4Threads)
     q4_dequantize_kernel(const uint8_t* __restrict__ in, Q4Layout L, void* __restrict__ out,
-                         uint64_t ld, bool vec, int32_t* status) {
+                         uint64_t ld, uint32_t vec, int32_t* status) {
     extern __shared__ __align__(16) uint8_t sm[];
     const uint32_t lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const uint32_t b0 = blockIdx.y * 8, s = blockIdx.x;
@@ -192,7 +266,7 @@ __global__ void __launch_bounds__(kQ4Threads)
             f[e] = sc * float(int((word >> (4 * ((e >> 1) + 4 * (e & 1)))) & 15u) - z);
         if (DT == 2) {
             float* o = static_cast<float*>(out) + uint64_t(row) * ld + c;
-            if (vec && c + 8 <= L.cols) {
+            if (vec == 16 && c + 8 <= L.cols) {
                 st_stream_v4(o, make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]),
                                            __float_as_uint(f[2]), __float_as_uint(f[3])));
                 st_stream_v4(o + 4, make_uint4(__float_as_uint(f[4]), __float_as_uint(f[5]),
@@ -203,24 +277,20 @@ __global__ void __launch_bounds__(kQ4Threads)
                     if (c + e < L.cols) o[e] = f[e];
             }
         } else {
-            uint16_t* o = static_cast<uint16_t*>(out) + uint64_t(row) * ld + c;
             uint16_t b[8];
 #pragma unroll
             for (int e = 0; e < 8; ++e) b[e] = from_float<DT == 1>(f[e]);
-            if (vec && c + 8 <= L.cols) {
-                st_stream_v4(o, make_uint4(b[0] | uint32_t(b[1]) << 16, b[2] | uint32_t(b[3]) << 16,
-                                           b[4] | uint32_t(b[5]) << 16, b[6] | uint32_t(b[7]) << 16));
-            } else {
-#pragma unroll
-                for (uint32_t e = 0; e < 8; ++e)
-                    if (c + e < L.cols) o[e] = b[e];
-            }
+            store8(static_cast<uint16_t*>(out) + uint64_t(row) * ld, c, L.cols, vec,
+                   make_uint4(b[0] | uint32_t(b[1]) << 16, b[2] | uint32_t(b[3]) << 16,
+                              b[4] | uint32_t(b[5]) << 16, b[6] | uint32_t(b[7]) << 16));
         }
     }
 }
 
-bool vec_ok(const void* p, uint64_t ld, uint32_t size) {
-    return (reinterpret_cast<uintptr_t>(p) & 15u) == 0 && (ld * size) % 16u == 0;
+// Bytes (2 to 16) that divide the address of every row.
+uint32_t row_align(const void* p, uint64_t ld, uint32_t size) {
+    const uint64_t a = reinterpret_cast<uintptr_t>(p) | (ld * size);
+    return a % 16 == 0 ? 16u : a % 8 == 0 ? 8u : a % 4 == 0 ? 4u : 2u;
 }
 
 dim3 q4_grid(const Q4Layout& L) { return dim3(L.slices, (L.blocks16 + 7) / 8); }
@@ -238,7 +308,7 @@ cudaError_t launch_q4_quantize(const void* w, uint64_t ld, const Q4Layout& L, ui
     }
     const auto kernel = L.half_scales ? q4_quantize_kernel<true> : q4_quantize_kernel<false>;
     kernel<<<q4_grid(L), kQ4Threads, 8 * kMaxRec, stream>>>(static_cast<const uint16_t*>(w), ld, L,
-                                                            vec_ok(w, ld, 2), out);
+                                                            row_align(w, ld, 2), out);
     return cudaGetLastError();
 }
 
@@ -260,7 +330,7 @@ cudaError_t launch_q4_dequantize(const uint8_t* in, const Q4Layout& L, void* out
                         : dtype == 1 ? q4_dequantize_kernel<1>
                                      : q4_dequantize_kernel<0>;
     kernel<<<q4_grid(L), kQ4Threads, 8 * kMaxRec, stream>>>(in, L, out, ld,
-                                                            vec_ok(out, ld, dtype == 2 ? 4 : 2), status);
+                                                            row_align(out, ld, dtype == 2 ? 4 : 2), status);
     return cudaGetLastError();
 }
 
