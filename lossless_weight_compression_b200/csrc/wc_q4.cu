@@ -72,24 +72,49 @@ __device__ __forceinline__ void store8(uint16_t* row, uint32_t c, uint32_t cols,
 }
 
 // Adding and subtracting 1.5 * 2^23 rounds |x| < 2^22 to the nearest integer,
-// ties to even, on the FMA pipe; after the addition the integer sits in the low
-// mantissa bits. (rintf and the conversion to int run at an eighth of its rate:
-// with them and a division a weight the kernel was bound by that unit.)
+// ties to even, on the FMA pipe (rintf and conversions to int run at an eighth of
+// its rate; with them and a division a weight that unit bound the kernel).
 constexpr float kRound = 12582912.f;
 
-// rint(w / s) as a float, r = 1 / s rounded. The quotient of the 16-bit values w
-// and s, each an integer of at most 11 bits times a power of two, is either a
-// tie k + 1/2 or at least 2^-13 away from every tie: with s = S 2^b, w = W 2^a,
-// w / s - (2 k + 1) / 2 = (2 W 2^(a-b) - (2 k + 1) S) / (2 S), whose numerator is
-// a multiple of 1/2 (w / s >= 1/4 makes a - b >= -2 for normalised W and S of
-// equal length) and S < 2^11. w * r is off by less than 2^-22 of itself, below
-// 2^-17 for quotients up to 32; so one within 2^-15 of a half-integer is that
-// half-integer, and rounds as the exact quotient does.
-__device__ __forceinline__ float quotient(float w, float r) {
+__device__ __forceinline__ float approx_rcp(float s) {
+    float r;
+    asm("rcp.approx.f32 %0, %1;" : "=f"(r) : "f"(s));
+    return r;
+}
+
+// w / s to within a rounding, and exactly where the quotient is a half-integer
+// up to 32: t = w r with r near 1 / s is off by a few 2^-23 of itself; the
+// remainder w - t s is exact by FMA (its bits lie between 2^-20 and 2^-35 of w,
+// s having at most 11), and adding r times it (a Newton step on the remainder)
+// leaves 2^-40 of the quotient before the last rounding, which a quotient that
+// FP32 holds absorbs. So the quotient rounds to the integer that the exact one
+// rounds to: with s = S 2^b and w = W 2^a, W and S of equal length below 2^11, it
+// is a half-integer or at least 2^-13 away from each: w / s - (2 k + 1) / 2 =
+// (2 W 2^(a-b) - (2 k + 1) S) / (2 S), whose numerator is a multiple of 1/2 where
+// w / s is near 1/2 or above (a - b >= -2).
+__device__ __forceinline__ float quotient(float w, float s, float r) {
     const float t = w * r;
-    const float h = fmaf(t, 2.f, kRound) - kRound;  // rint(2 t)
-    const float half = 0.5f * h;
-    return fabsf(t - half) < 3.0517578125e-5f ? half : t;
+    return fmaf(fmaf(-t, s, w), r, t);
+}
+
+// The larger (smaller) of two pairs of 16-bit floats; NaN if either is.
+template <bool HALF>
+__device__ __forceinline__ uint32_t max2(uint32_t a, uint32_t b) {
+    uint32_t d;
+    if (HALF)
+        asm("max.NaN.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+    else
+        asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+    return d;
+}
+template <bool HALF>
+__device__ __forceinline__ uint32_t min2(uint32_t a, uint32_t b) {
+    uint32_t d;
+    if (HALF)
+        asm("min.NaN.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+    else
+        asm("min.NaN.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+    return d;
 }
 
 // The word of eight codes in element order.
@@ -116,9 +141,9 @@ __device__ __forceinline__ void store_header(const Q4Layout& L, uint8_t* out) {
 //   without zero points  s = rnd16(max|w| / 7), q = clamp(rint(w / s), -8, 7) + 8
 //   with zero points     lo = min(w, 0), hi = max(w, 0), s = rnd16((hi - lo) / 15),
 //                        z = clamp(rint(-lo / s), 0, 15), q = clamp(rint(w / s) + z, 0, 15)
-// (s = 0: every code stands for zero). The quotients are FP32 with one rounding;
-// w and s have at most 11 significant bits, so no quotient that is not a tie in
-// exact arithmetic comes within an FP32 rounding of one.
+// (s = 0: every code stands for zero). The range is reduced as one pair of 16-bit
+// floats a lane, max(w, 0) and max(-w, 0); the codes of four elements add up as
+// 16^k-weighted floats (below 2^16, exact).
 template <bool HALF>
 __global__ void __launch_bounds__(kQ4Threads)
     q4_quantize_kernel(const uint16_t* __restrict__ w, uint64_t ld, Q4Layout L, uint32_t vec,
@@ -142,51 +167,51 @@ __global__ void __launch_bounds__(kQ4Threads)
 #pragma unroll
         for (uint32_t k = 0; k < 8; ++k) {
             const uint32_t r = 2 * k + (lane >> 4);
-            float f[8];
             const uint32_t u[4] = {v[k].x, v[k].y, v[k].z, v[k].w};
-#pragma unroll
-            for (int e = 0; e < 8; ++e) f[e] = to_float<HALF>(uint16_t(u[e >> 1] >> (16 * (e & 1))));
-            // fminf and fmaxf drop a NaN, which has to reach the scale: it enters as
-            // both infinities
+            const uint32_t mx = max2<HALF>(max2<HALF>(u[0], u[1]), max2<HALF>(u[2], u[3]));
+            const uint32_t mn = min2<HALF>(min2<HALF>(u[0], u[1]), min2<HALF>(u[2], u[3])) ^
+                                0x80008000u;  // negated: the largest -w
+            // {even w, even -w} against {odd w, odd -w}, and 0
+            uint32_t m = max2<HALF>(prmt(mx, mn, 0x5410u), prmt(mx, mn, 0x7632u));
+            m = max2<HALF>(m, 0u);
+            for (uint32_t o = 1; o < lanes; o *= 2)
+                m = max2<HALF>(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
+            const float hi = to_float<HALF>(uint16_t(m)), lo = to_float<HALF>(uint16_t(m >> 16));
+            // (a NaN made both NaN; infinities of both signs count as one)
             const float inf = __int_as_float(0x7F800000);
-            float lo = 0.f, hi = 0.f;
-            bool nan = false;
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                lo = fminf(lo, f[e]);
-                hi = fmaxf(hi, f[e]);
-                nan |= f[e] != f[e];
-            }
-            if (nan) hi = inf, lo = -inf;
-            for (uint32_t o = 1; o < lanes; o *= 2) {
-                lo = fminf(lo, __shfl_xor_sync(0xFFFFFFFFu, lo, o));
-                hi = fmaxf(hi, __shfl_xor_sync(0xFFFFFFFFu, hi, o));
-            }
-            float range = L.zeros ? hi - lo : fmaxf(hi, -lo);
-            if (hi == inf && lo == -inf) range = __int_as_float(0x7FC00000);
+            float range = L.zeros ? hi + lo : fmaxf(hi, lo);
+            if (hi != hi || (hi == inf && lo == inf)) range = __int_as_float(0x7FC00000);
             const uint16_t sbits = from_float<HALF>(range / steps);
             const float sc = to_float<HALF>(sbits);
-            uint32_t q[8];
+            uint32_t word;
             float z = 8.f;
             if (sc > 1e-30f && sc < 1e30f) {
-                const float r = 1.f / sc;
-                if (L.zeros) z = fminf((quotient(-lo, r) + kRound) - kRound, 15.f);
-                const float zk = z + kRound;
+                const float r = approx_rcp(sc);
+                if (L.zeros) z = fminf((quotient(lo, sc, r) + kRound) - kRound, 15.f);
+                const float zk = z - kRound, top = 15.f - z;
+                float part[2] = {0.f, 0.f};  // even and odd elements
 #pragma unroll
-                for (int e = 0; e < 8; ++e) {
+                for (int e = 7; e >= 0; --e) {
+                    const float f = to_float<HALF>(uint16_t(u[e >> 1] >> (16 * (e & 1))));
                     // clamped before the rounding: the bounds are integers
-                    const float t = fminf(fmaxf(quotient(f[e], r), -z), 15.f - z);
-                    q[e] = __float_as_uint((t + kRound) - kRound + zk) & 15u;
+                    const float t = fminf(fmaxf(quotient(f, sc, r), -z), top);
+                    part[e & 1] = fmaf(part[e & 1], 16.f, (t + kRound) + zk);
                 }
+                word = prmt(__float_as_uint(part[0] + 8388608.f), __float_as_uint(part[1] + 8388608.f),
+                            0x5410u);
             } else {  // no scale, one that 1 / s cannot hold, infinity or NaN: the definition's steps
                 const float d = sc > 0.f ? sc : 1.f;
-                if (L.zeros) z = fminf(fmaxf(rintf(-lo / d), 0.f), 15.f);
+                if (L.zeros) z = fminf(fmaxf(rintf(lo / d), 0.f), 15.f);
+                uint32_t q[8];
 #pragma unroll
-                for (int e = 0; e < 8; ++e)
-                    q[e] = uint32_t(fminf(fmaxf(rintf(f[e] / d) + z, 0.f), 15.f));
+                for (int e = 0; e < 8; ++e) {
+                    const float f = to_float<HALF>(uint16_t(u[e >> 1] >> (16 * (e & 1))));
+                    q[e] = uint32_t(fminf(fmaxf(rintf(f / d) + z, 0.f), 15.f));
+                }
+                word = pack8(q);
             }
             const uint32_t i = c8 >> 2, t = c8 & 3u;
-            *reinterpret_cast<uint32_t*>(rec + t * 256 + r * 16 + i * 4) = pack8(q);
+            *reinterpret_cast<uint32_t*>(rec + t * 256 + r * 16 + i * 4) = word;
             if ((c8 & (L.group / 8 - 1)) == 0) {
                 const uint32_t g = c8 / (L.group / 8);
                 *reinterpret_cast<uint16_t*>(rec + kQ4Codes + (g * 16 + r) * 2) = sbits;
@@ -259,11 +284,13 @@ __global__ void __launch_bounds__(kQ4Threads)
             *reinterpret_cast<const uint32_t*>(rec + (c8 & 3u) * 256 + r * 16 + (c8 >> 2) * 4);
         const float sc = q4_scale(*reinterpret_cast<const uint16_t*>(rec + kQ4Codes + (g * 16 + r) * 2),
                                   L.half_scales);
-        const int z = L.zeros ? int(rec[kQ4Codes + 32 * L.per + g * 16 + r] & 15u) : 8;
+        // 2^23 + q and 2^23 + z in the low mantissa bits: their difference is q - z
+        const float z = __uint_as_float(
+            0x4B000000u | (L.zeros ? rec[kQ4Codes + 32 * L.per + g * 16 + r] & 15u : 8u));
         float f[8];
 #pragma unroll
         for (int e = 0; e < 8; ++e)
-            f[e] = sc * float(int((word >> (4 * ((e >> 1) + 4 * (e & 1)))) & 15u) - z);
+            f[e] = sc * (__uint_as_float(((word >> (4 * ((e >> 1) + 4 * (e & 1)))) & 15u) | 0x4B000000u) - z);
         if (DT == 2) {
             float* o = static_cast<float*>(out) + uint64_t(row) * ld + c;
             if (vec == 16 && c + 8 <= L.cols) {

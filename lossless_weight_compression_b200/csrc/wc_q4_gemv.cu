@@ -162,7 +162,7 @@ __device__ __forceinline__ void slice_mma(const Slice<RT, NT, PER>& v, uint32_t 
 // that take the row group's slices in turns (the blocks of a cluster, too). The
 // next slice is on its way while one is multiplied.
 template <bool HALF, int RT, int NT, int PER>
-__global__ void __launch_bounds__(kGvThreads) q4_gemv_kernel(const __grid_constant__ GvParams P) {
+__global__ void __launch_bounds__(kGvThreads, 2) q4_gemv_kernel(const __grid_constant__ GvParams P) {
     const Q4Layout& L = P.L;
     const Q4GemmArgs& A = P.a;
     constexpr int kVals = RT * NT * 4 * 32;  // results of a row group, padding included

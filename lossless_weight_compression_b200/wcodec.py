@@ -12,6 +12,7 @@ allocate outputs with torch and call the same entry points.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 from dataclasses import dataclass
@@ -785,42 +786,64 @@ _DTYPES = {torch.bfloat16: WC_DTYPE_BF16, torch.float16: WC_DTYPE_FP16,
            torch.float32: WC_DTYPE_FP32}
 
 
-def _run_on(device: torch.device, stream, fn):
-    """fn(stream handle) with `device` current and `stream` (default: the
-    device's current stream) the one that tensors are allocated on."""
+_current_device = torch._C._cuda_getDevice if hasattr(torch._C, "_cuda_getDevice") \
+    else torch.cuda.current_device
+if hasattr(torch._C, "_cuda_getCurrentRawStream"):
+    _raw_stream = torch._C._cuda_getCurrentRawStream  # a fiftieth of current_stream()'s time
+else:
+    def _raw_stream(index):
+        return torch.cuda.current_stream(index).cuda_stream
+
+
+def _here(t: torch.Tensor, stream) -> bool:
+    """Whether t's device is the current one and its current stream is meant."""
+    return t.is_cuda and stream is None and t.get_device() == _current_device()
+
+
+@contextlib.contextmanager
+def _there(device: torch.device, stream):
+    """Make ``device`` current, and ``stream`` (if given) the one that work is
+    enqueued and tensors are allocated on."""
     if device.type != "cuda":
         raise ValueError("wcodec works on CUDA tensors; got one on %s" % device)
-    if stream is None and device.index == torch.cuda.current_device():
-        return fn(torch.cuda.current_stream().cuda_stream)
     with torch.cuda.device(device):
         if stream is None:
-            return fn(torch.cuda.current_stream().cuda_stream)
-        with torch.cuda.stream(stream):
-            return fn(stream.cuda_stream)
+            yield
+        else:
+            with torch.cuda.stream(stream):
+                yield
 
 
-def _rows(t: torch.Tensor, cols: int, what: str, device=None) -> torch.Tensor:
-    """A matrix of `cols` columns whose rows are dense (they may lie apart)."""
-    if t.dim() != 2 or t.shape[1] != cols:
-        raise ValueError("%s must be a matrix of %d columns; got %s" % (what, cols, tuple(t.shape)))
+def _rows(t: torch.Tensor, cols: int, what: str, device=None) -> int:
+    """Check a matrix of `cols` columns whose rows are dense (they may lie
+    apart); returns the elements between rows."""
+    shape = t.shape
+    if len(shape) != 2 or shape[1] != cols:
+        raise ValueError("%s must be a matrix of %d columns; got %s" % (what, cols, tuple(shape)))
     if device is not None and t.device != device:
         raise ValueError("%s is on %s, not on %s" % (what, t.device, device))
-    if t.numel() and ((cols > 1 and t.stride(1) != 1)
-                      or (t.shape[0] > 1 and t.stride(0) < cols)):
+    rows = shape[0]
+    if rows == 0 or cols == 0:
+        return cols
+    ld, inner = t.stride()
+    if (cols > 1 and inner != 1) or (rows > 1 and ld < cols):
         raise ValueError("%s must have dense rows; got strides %s" % (what, t.stride()))
-    return t
-
-
-def _ld(t: torch.Tensor) -> int:
-    """Elements between rows (the stride of a single row or of none means nothing)."""
-    return t.stride(0) if t.shape[0] > 1 and t.numel() else t.shape[1]
+    return ld if rows > 1 else cols  # the stride of a single row means nothing
 
 
 def _vector(t: torch.Tensor, shape: tuple, dtype: torch.dtype, what: str, device) -> torch.Tensor:
-    if tuple(t.shape) != shape or t.dtype != dtype or t.device != device or not t.is_contiguous():
+    if t.shape != shape or t.dtype != dtype or t.device != device or not t.is_contiguous():
         raise ValueError("%s must be a contiguous %s tensor of shape %s on %s"
-                         % (what, dtype, shape, device))
+                         % (what, dtype, tuple(shape), device))
     return t
+
+
+def _status_ptr(status: torch.Tensor | None, device):
+    if status is None:
+        return None
+    if status.dtype != torch.int32 or status.numel() < 1 or status.device != device:
+        raise ValueError("status must be an int32 tensor on %s" % device)
+    return status.data_ptr()
 
 
 @dataclass
@@ -835,10 +858,11 @@ class Q4Matrix:
     scale_dtype: torch.dtype
 
     def flags(self) -> int:
-        if self.scale_dtype not in (torch.bfloat16, torch.float16):
-            raise TypeError("scales are BF16 or FP16; got %s" % self.scale_dtype)
-        return (WC_Q4_ZEROS if self.zeros else 0) | (
-            WC_Q4_SCALES_FP16 if self.scale_dtype == torch.float16 else 0)
+        if self.scale_dtype == torch.bfloat16:
+            return WC_Q4_ZEROS if self.zeros else 0
+        if self.scale_dtype == torch.float16:
+            return WC_Q4_SCALES_FP16 + (WC_Q4_ZEROS if self.zeros else 0)
+        raise TypeError("scales are BF16 or FP16; got %s" % self.scale_dtype)
 
 
 def _q4_buffer(m: Q4Matrix, dims: int) -> torch.Tensor:
@@ -857,35 +881,43 @@ def _q4_size(rows: int, cols: int, group: int, flags: int) -> int:
     return size
 
 
+def _q4_out(m: Q4Matrix, size: int, like: torch.Tensor) -> torch.Tensor:
+    if m.buffer is None:
+        m.buffer = like.new_empty(size, dtype=torch.uint8)
+    elif m.buffer.device != like.device:
+        raise ValueError("out is on %s, not on %s" % (m.buffer.device, like.device))
+    return _q4_buffer(m, 1)
+
+
 def quantize_q4(w: torch.Tensor, group: int = 128, *, zeros: bool = False,
                 out: torch.Tensor | None = None, stream=None) -> Q4Matrix:
     """Round a BF16 or FP16 matrix to a 4-bit stream with one scale of its type
     (and with ``zeros`` a zero point) per row and ``group`` columns."""
-    if w.dtype not in (torch.bfloat16, torch.float16):
+    if w.dtype != torch.bfloat16 and w.dtype != torch.float16:
         raise TypeError("quantize_q4 takes BF16 or FP16; got %s" % w.dtype)
-    rows, cols = _rows(w, w.shape[-1], "w").shape
+    if w.dim() != 2:
+        raise ValueError("w must be a matrix; got shape %s" % (tuple(w.shape),))
+    rows, cols = w.shape
+    ld = _rows(w, cols, "w")
     m = Q4Matrix(out, rows, cols, group, zeros, w.dtype)
     flags = m.flags()
     size = _q4_size(rows, cols, group, flags)
-
-    def run(handle):
-        if m.buffer is None:
-            m.buffer = torch.empty(size, dtype=torch.uint8, device=w.device)
-        elif m.buffer.device != w.device:
-            raise ValueError("out is on %s, not on %s" % (m.buffer.device, w.device))
-        b = _q4_buffer(m, 1)
-        _check(wc_q4_quantize(w.data_ptr(), _ld(w), rows, cols, group, flags, b.data_ptr(),
-                              b.numel(), handle), "wc_q4_quantize")
-        return m
-    return _run_on(w.device, stream, run)
+    if not _here(w, stream):
+        with _there(w.device, stream):
+            return quantize_q4(w, group, zeros=zeros, out=out)
+    b = _q4_out(m, size, w)
+    rc = lib().wc_q4_quantize(w.data_ptr(), ld, rows, cols, group, flags, b.data_ptr(), b.numel(),
+                              _raw_stream(w.get_device()))
+    _check(rc, "wc_q4_quantize")
+    return m
 
 
 def pack_q4(codes: torch.Tensor, scales: torch.Tensor, zeros: torch.Tensor | None = None, *,
             group: int = 128, out: torch.Tensor | None = None, stream=None) -> Q4Matrix:
     """The stream of given codes (uint8, rows x cols, 0..15), scales (BF16 or
     FP16, rows x ceil(cols / group)) and zero points (uint8, as the scales)."""
-    if codes.dim() != 2 or codes.device.type != "cuda":
-        raise ValueError("codes must be a CUDA matrix")
+    if codes.dim() != 2:
+        raise ValueError("codes must be a matrix; got shape %s" % (tuple(codes.shape),))
     rows, cols = codes.shape
     m = Q4Matrix(out, rows, cols, group, zeros is not None, scales.dtype)
     flags = m.flags()
@@ -895,18 +927,15 @@ def pack_q4(codes: torch.Tensor, scales: torch.Tensor, zeros: torch.Tensor | Non
     _vector(scales, shape, scales.dtype, "scales", codes.device)
     if zeros is not None:
         _vector(zeros, shape, torch.uint8, "zeros", codes.device)
-
-    def run(handle):
-        if m.buffer is None:
-            m.buffer = torch.empty(size, dtype=torch.uint8, device=codes.device)
-        elif m.buffer.device != codes.device:
-            raise ValueError("out is on %s, not on %s" % (m.buffer.device, codes.device))
-        b = _q4_buffer(m, 1)
-        _check(wc_q4_pack(codes.data_ptr(), scales.data_ptr(),
+    if not _here(codes, stream):
+        with _there(codes.device, stream):
+            return pack_q4(codes, scales, zeros, group=group, out=out)
+    b = _q4_out(m, size, codes)
+    rc = lib().wc_q4_pack(codes.data_ptr(), scales.data_ptr(),
                           None if zeros is None else zeros.data_ptr(), rows, cols, group, flags,
-                          b.data_ptr(), b.numel(), handle), "wc_q4_pack")
-        return m
-    return _run_on(codes.device, stream, run)
+                          b.data_ptr(), b.numel(), _raw_stream(codes.get_device()))
+    _check(rc, "wc_q4_pack")
+    return m
 
 
 def dequantize_q4(m: Q4Matrix, dtype: torch.dtype = torch.bfloat16, *,
@@ -914,53 +943,49 @@ def dequantize_q4(m: Q4Matrix, dtype: torch.dtype = torch.bfloat16, *,
                   stream=None) -> torch.Tensor:
     """The weights of a 4-bit stream, rounded once to ``dtype`` (BF16, FP16 or FP32)."""
     b = _q4_buffer(m, 1)
+    rows, cols = m.rows, m.cols
+    ld = cols
     if out is not None:
-        dtype = _rows(out, m.cols, "out", b.device).dtype
-        if out.shape[0] != m.rows:
-            raise ValueError("out must have %d rows" % m.rows)
+        ld = _rows(out, cols, "out", b.device)
+        dtype = out.dtype
+        if out.shape[0] != rows:
+            raise ValueError("out must have %d rows" % rows)
     if dtype not in _DTYPES:
         raise TypeError("dequantize_q4 gives BF16, FP16 or FP32; got %s" % dtype)
+    if not _here(b, stream):
+        with _there(b.device, stream):
+            return dequantize_q4(m, dtype, out=out, status=status)
+    if out is None:
+        out = b.new_empty((rows, cols), dtype=dtype)
+    rc = lib().wc_q4_dequantize(b.data_ptr(), b.numel(), rows, cols, m.group, m.flags(),
+                                out.data_ptr(), ld, _DTYPES[dtype], _status_ptr(status, b.device),
+                                _raw_stream(b.get_device()))
+    _check(rc, "wc_q4_dequantize")
+    return out
 
-    def run(handle):
-        o = torch.empty((m.rows, m.cols), dtype=dtype, device=b.device) if out is None else out
-        _check(wc_q4_dequantize(b.data_ptr(), b.numel(), m.rows, m.cols, m.group, m.flags(),
-                                o.data_ptr(), _ld(o), _DTYPES[dtype],
-                                None if status is None else status.data_ptr(), handle),
-               "wc_q4_dequantize")
-        return o
-    return _run_on(b.device, stream, run)
 
-
-def _q4_product(m: Q4Matrix, b, x, offsets, y, out_dtype, status, stream):
-    if x.dtype not in (torch.bfloat16, torch.float16):
-        raise TypeError("activations are BF16 or FP16; got %s" % x.dtype)
-    _rows(x, m.cols, "x", b.device)
+def _q4_product_args(m: Q4Matrix, b, x, y, out_dtype):
+    """Checks shared by the two products: (tokens, ldx, ldy, flags, result type)."""
+    dt = x.dtype
+    if dt == torch.bfloat16:
+        flags = m.flags()
+    elif dt == torch.float16:
+        flags = m.flags() + WC_Q4_X_FP16
+    else:
+        raise TypeError("activations are BF16 or FP16; got %s" % dt)
+    ldx = _rows(x, m.cols, "x", b.device)
     tokens = x.shape[0]
+    ldy = m.rows
     if y is not None:
-        out_dtype = _rows(y, m.rows, "y", b.device).dtype
+        ldy = _rows(y, m.rows, "y", b.device)
+        out_dtype = y.dtype
         if y.shape[0] != tokens:
             raise ValueError("y must have %d rows" % tokens)
-    if out_dtype != torch.float32 and out_dtype != x.dtype:
-        raise TypeError("the product is FP32 or has x's type; got %s" % out_dtype)
-    flags = m.flags() | (WC_Q4_X_FP16 if x.dtype == torch.float16 else 0) | (
-        0 if out_dtype == torch.float32 else WC_Q4_Y_16BIT)
-
-    def run(handle):
-        o = torch.empty((tokens, m.rows), dtype=out_dtype, device=b.device) if y is None else y
-        st = None if status is None else status.data_ptr()
-        if offsets is None:
-            rc = lib().wc_q4_gemm(b.data_ptr(), b.numel(), m.rows, m.cols, m.group, flags,
-                                  x.data_ptr(), _ld(x), tokens, o.data_ptr(), _ld(o), st, handle)
-            _check(rc, "wc_q4_gemm")
-        else:
-            rc = lib().wc_q4_gemm_experts(b.data_ptr(),
-                                          b.stride(0) if b.shape[0] > 1 else b.shape[1],
-                                          b.shape[0], m.rows, m.cols, m.group, flags, x.data_ptr(),
-                                          _ld(x), tokens, offsets.data_ptr(), o.data_ptr(), _ld(o),
-                                          st, handle)
-            _check(rc, "wc_q4_gemm_experts")
-        return o
-    return _run_on(b.device, stream, run)
+    if out_dtype != torch.float32:
+        if out_dtype != dt:
+            raise TypeError("the product is FP32 or has x's type; got %s" % out_dtype)
+        flags += WC_Q4_Y_16BIT
+    return tokens, ldx, ldy, flags, out_dtype
 
 
 def gemm_q4(m: Q4Matrix, x: torch.Tensor, *, y: torch.Tensor | None = None,
@@ -968,7 +993,19 @@ def gemm_q4(m: Q4Matrix, x: torch.Tensor, *, y: torch.Tensor | None = None,
             stream=None) -> torch.Tensor:
     """y = x @ W.T with W held as a 4-bit stream; x is (tokens, cols) BF16 or
     FP16, y (tokens, rows) in FP32 or x's type."""
-    return _q4_product(m, _q4_buffer(m, 1), x, None, y, out_dtype, status, stream)
+    b = _q4_buffer(m, 1)
+    tokens, ldx, ldy, flags, out_dtype = _q4_product_args(m, b, x, y, out_dtype)
+    if not _here(b, stream):
+        with _there(b.device, stream):
+            return gemm_q4(m, x, y=y, out_dtype=out_dtype, status=status)
+    if y is None:
+        y = x.new_empty((tokens, m.rows), dtype=out_dtype)
+    rc = lib().wc_q4_gemm(b.data_ptr(), b.numel(), m.rows, m.cols, m.group, flags, x.data_ptr(),
+                          ldx, tokens, y.data_ptr(), ldy,
+                          None if status is None else _status_ptr(status, b.device),
+                          _raw_stream(b.get_device()))
+    _check(rc, "wc_q4_gemm")
+    return y
 
 
 def gemm_q4_experts(m: Q4Matrix, x: torch.Tensor, offsets: torch.Tensor, *,
@@ -978,8 +1015,21 @@ def gemm_q4_experts(m: Q4Matrix, x: torch.Tensor, offsets: torch.Tensor, *,
     offsets[e + 1] - 1 of x take matrix e (offsets int32, as moe_sort gives
     them). Rows outside every range are left as they were in ``y``."""
     b = _q4_buffer(m, 2)
-    _vector(offsets, (b.shape[0] + 1,), torch.int32, "offsets", b.device)
-    return _q4_product(m, b, x, offsets, y, out_dtype, status, stream)
+    experts, size = b.shape
+    _vector(offsets, (experts + 1,), torch.int32, "offsets", b.device)
+    tokens, ldx, ldy, flags, out_dtype = _q4_product_args(m, b, x, y, out_dtype)
+    if not _here(b, stream):
+        with _there(b.device, stream):
+            return gemm_q4_experts(m, x, offsets, y=y, out_dtype=out_dtype, status=status)
+    if y is None:
+        y = x.new_empty((tokens, m.rows), dtype=out_dtype)
+    rc = lib().wc_q4_gemm_experts(b.data_ptr(), b.stride(0) if experts > 1 else size, experts,
+                                  m.rows, m.cols, m.group, flags, x.data_ptr(), ldx, tokens,
+                                  offsets.data_ptr(), y.data_ptr(), ldy,
+                                  None if status is None else _status_ptr(status, b.device),
+                                  _raw_stream(b.get_device()))
+    _check(rc, "wc_q4_gemm_experts")
+    return y
 
 
 @dataclass
@@ -995,24 +1045,25 @@ class MoePlan:
 def moe_sort(ids: torch.Tensor, experts: int, *, stream=None) -> MoePlan:
     """The plan that sorts (token, choice) slots by expert: ids is (tokens, top)
     int32; ids outside 0..experts-1 are dropped."""
-    if ids.dim() != 2:
-        raise ValueError("ids must be (tokens, top)")
-    _vector(ids, tuple(ids.shape), torch.int32, "ids", ids.device)
+    if ids.dim() != 2 or ids.dtype != torch.int32 or not ids.is_contiguous():
+        raise ValueError("ids must be a contiguous int32 tensor of shape (tokens, top)")
     if not 1 <= experts <= WC_MOE_MAX_EXPERTS:
         raise ValueError("1 to %d experts; got %r" % (WC_MOE_MAX_EXPERTS, experts))
+    if not _here(ids, stream):
+        with _there(ids.device, stream):
+            return moe_sort(ids, experts)
+    slots = ids.numel()
+    offsets = ids.new_empty(experts + 1)
+    order = ids.new_empty(slots)
+    inverse = ids.new_empty(ids.shape)
+    rc = lib().wc_moe_sort(ids.data_ptr(), slots, experts, offsets.data_ptr(), order.data_ptr(),
+                           inverse.data_ptr(), _raw_stream(ids.get_device()))
+    _check(rc, "wc_moe_sort")
+    return MoePlan(offsets, order, inverse)
 
-    def run(handle):
-        slots = ids.numel()
-        offsets = torch.empty(experts + 1, dtype=torch.int32, device=ids.device)
-        order = torch.empty(slots, dtype=torch.int32, device=ids.device)
-        inverse = torch.empty_like(ids)
-        _check(lib().wc_moe_sort(ids.data_ptr(), slots, experts, offsets.data_ptr(),
-                                 order.data_ptr(), inverse.data_ptr(), handle), "wc_moe_sort")
-        return MoePlan(offsets, order, inverse)
-    return _run_on(ids.device, stream, run)
 
-
-def _moe_check(t: torch.Tensor, cols: int, what: str, like: torch.Tensor):
+def _moe_matrix(t: torch.Tensor, cols: int, what: str, like: torch.Tensor) -> int:
+    """Check a matrix of the routing operators; returns the elements between rows."""
     if t.dtype not in _DTYPES or t.dtype != like.dtype:
         raise TypeError("%s must be BF16, FP16 or FP32 and of one type; got %s" % (what, t.dtype))
     return _rows(t, cols, what, like.device)
@@ -1022,7 +1073,7 @@ def _moe_inverse(plan: MoePlan, device) -> torch.Tensor:
     inv = plan.inverse
     if inv.dim() != 2:
         raise ValueError("plan.inverse must be (tokens, top)")
-    return _vector(inv, tuple(inv.shape), torch.int32, "plan.inverse", device)
+    return _vector(inv, inv.shape, torch.int32, "plan.inverse", device)
 
 
 def moe_gather(x: torch.Tensor, plan: MoePlan, *, out: torch.Tensor | None = None,
@@ -1032,44 +1083,48 @@ def moe_gather(x: torch.Tensor, plan: MoePlan, *, out: torch.Tensor | None = Non
     inv = _moe_inverse(plan, x.device)
     tokens, top = inv.shape
     cols = x.shape[-1]
-    _moe_check(x, cols, "x", x)
+    ldx = _moe_matrix(x, cols, "x", x)
     if x.shape[0] != tokens:
         raise ValueError("x must have %d rows" % tokens)
-    if out is not None:
-        _moe_check(out, cols, "out", x)
-
-    def run(handle):
-        o = torch.empty((tokens * top, cols), dtype=x.dtype, device=x.device) if out is None else out
-        _check(lib().wc_moe_gather(x.data_ptr(), _ld(x), tokens, top, cols, _DTYPES[x.dtype],
-                                   inv.data_ptr(), o.data_ptr(), _ld(o), o.shape[0], handle),
-               "wc_moe_gather")
-        return o
-    return _run_on(x.device, stream, run)
+    ldo = cols if out is None else _moe_matrix(out, cols, "out", x)
+    if not _here(x, stream):
+        with _there(x.device, stream):
+            return moe_gather(x, plan, out=out)
+    if out is None:
+        out = x.new_empty((tokens * top, cols))
+    rc = lib().wc_moe_gather(x.data_ptr(), ldx, tokens, top, cols, _DTYPES[x.dtype], inv.data_ptr(),
+                             out.data_ptr(), ldo, out.shape[0], _raw_stream(x.get_device()))
+    _check(rc, "wc_moe_gather")
+    return out
 
 
 def moe_combine(rows: torch.Tensor, plan: MoePlan, weights: torch.Tensor | None, *,
                 out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """out[t] = sum_j weights[t, j] * rows[plan.inverse[t, j]] (weights FP32,
     None: all 1), in the type of rows."""
-    inv = _moe_inverse(plan, rows.device)
+    device = rows.device
+    inv = _moe_inverse(plan, device)
     tokens, top = inv.shape
     cols = rows.shape[-1]
-    _moe_check(rows, cols, "rows", rows)
+    ldr = _moe_matrix(rows, cols, "rows", rows)
     if weights is not None:
-        _vector(weights, (tokens, top), torch.float32, "weights", rows.device)
+        _vector(weights, inv.shape, torch.float32, "weights", device)
+    ldo = cols
     if out is not None:
-        _moe_check(out, cols, "out", rows)
+        ldo = _moe_matrix(out, cols, "out", rows)
         if out.shape[0] != tokens:
             raise ValueError("out must have %d rows" % tokens)
-
-    def run(handle):
-        o = torch.empty((tokens, cols), dtype=rows.dtype, device=rows.device) if out is None else out
-        _check(lib().wc_moe_combine(rows.data_ptr(), _ld(rows), rows.shape[0], tokens, top, cols,
-                                    _DTYPES[rows.dtype], inv.data_ptr(),
-                                    None if weights is None else weights.data_ptr(), o.data_ptr(),
-                                    _ld(o), handle), "wc_moe_combine")
-        return o
-    return _run_on(rows.device, stream, run)
+    if not _here(rows, stream):
+        with _there(device, stream):
+            return moe_combine(rows, plan, weights, out=out)
+    if out is None:
+        out = rows.new_empty((tokens, cols))
+    rc = lib().wc_moe_combine(rows.data_ptr(), ldr, rows.shape[0], tokens, top, cols,
+                              _DTYPES[rows.dtype], inv.data_ptr(),
+                              None if weights is None else weights.data_ptr(), out.data_ptr(), ldo,
+                              _raw_stream(rows.get_device()))
+    _check(rc, "wc_moe_combine")
+    return out
 
 
 def moe_gather_backward(drows: torch.Tensor, plan: MoePlan, *, out: torch.Tensor | None = None,
@@ -1083,28 +1138,30 @@ def moe_combine_backward(dout: torch.Tensor, rows: torch.Tensor, plan: MoePlan,
                          stream=None) -> tuple[torch.Tensor, torch.Tensor]:
     """The gradients of moe_combine's rows and weights. Rows that no slot names
     are left as they were in ``drows``."""
-    inv = _moe_inverse(plan, rows.device)
+    device = rows.device
+    inv = _moe_inverse(plan, device)
     tokens, top = inv.shape
     cols = rows.shape[-1]
-    _moe_check(rows, cols, "rows", rows)
-    _moe_check(dout, cols, "dout", rows)
+    ldr = _moe_matrix(rows, cols, "rows", rows)
+    ldd = _moe_matrix(dout, cols, "dout", rows)
     if dout.shape[0] != tokens:
         raise ValueError("dout must have %d rows" % tokens)
     if weights is not None:
-        _vector(weights, (tokens, top), torch.float32, "weights", rows.device)
+        _vector(weights, inv.shape, torch.float32, "weights", device)
+    lddr = cols
     if drows is not None:
-        _moe_check(drows, cols, "drows", rows)
+        lddr = _moe_matrix(drows, cols, "drows", rows)
         if drows.shape[0] != rows.shape[0]:
             raise ValueError("drows must have %d rows" % rows.shape[0])
-
-    def run(handle):
-        d = (torch.empty((rows.shape[0], cols), dtype=rows.dtype, device=rows.device)
-             if drows is None else drows)
-        dw = torch.empty((tokens, top), dtype=torch.float32, device=rows.device)
-        _check(lib().wc_moe_combine_backward(
-            dout.data_ptr(), _ld(dout), rows.data_ptr(), _ld(rows), rows.shape[0], tokens, top,
-            cols, _DTYPES[rows.dtype], inv.data_ptr(),
-            None if weights is None else weights.data_ptr(), d.data_ptr(), _ld(d), dw.data_ptr(),
-            handle), "wc_moe_combine_backward")
-        return d, dw
-    return _run_on(rows.device, stream, run)
+    if not _here(rows, stream):
+        with _there(device, stream):
+            return moe_combine_backward(dout, rows, plan, weights, drows=drows)
+    if drows is None:
+        drows = rows.new_empty((rows.shape[0], cols))
+    dweights = rows.new_empty((tokens, top), dtype=torch.float32)
+    rc = lib().wc_moe_combine_backward(
+        dout.data_ptr(), ldd, rows.data_ptr(), ldr, rows.shape[0], tokens, top, cols,
+        _DTYPES[rows.dtype], inv.data_ptr(), None if weights is None else weights.data_ptr(),
+        drows.data_ptr(), lddr, dweights.data_ptr(), _raw_stream(rows.get_device()))
+    _check(rc, "wc_moe_combine_backward")
+    return drows, dweights
