@@ -480,7 +480,7 @@ int wc_decompress_tans_batch(const wc_batch_item *h_items, uint32_t count, int32
  *  wc_q4_quantize    rounds rows x cols 16-bit weights (rows ld elements apart,
  *                    2-byte aligned; BF16, or FP16 with WC_Q4_SCALES_FP16: the
  *                    scales have the weights' type) to a stream at d_out. Per
- *                    row and group, to nearest even:
+ *                    row and group, to nearest even (ranges in FP32):
  *                      s = round16(max|w| / 7), q = clamp(rint(w/s), -8, 7) + 8
  *                    or, with WC_Q4_ZEROS, lo = min(w, 0), hi = max(w, 0),
  *                      s = round16((hi - lo) / 15), z = clamp(rint(-lo/s), 0, 15),

@@ -25,6 +25,17 @@ __device__ __forceinline__ uint16_t from_float(float v) {
     return HALF ? __half_as_ushort(__float2half_rn(v)) : __bfloat16_as_ushort(__float2bfloat16_rn(v));
 }
 
+// Two values rounded to 16 bits, the first in the low half.
+template <bool HALF>
+__device__ __forceinline__ uint32_t pack2(float a, float b) {
+    uint32_t d;
+    if (HALF)
+        asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(b), "f"(a));
+    else
+        asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(b), "f"(a));
+    return d;
+}
+
 // Eight consecutive 16-bit values of a row from column c, zeros past the end.
 // `vec`: bytes that divide the address of every row (2 to 16).
 __device__ __forceinline__ uint4 load8(const uint16_t* row, uint32_t c, uint32_t cols, bool live,
@@ -144,29 +155,57 @@ __device__ __forceinline__ void store_header(const Q4Layout& L, uint8_t* out) {
 // (s = 0: every code stands for zero). The range is reduced as one pair of 16-bit
 // floats a lane, max(w, 0) and max(-w, 0); the codes of four elements add up as
 // 16^k-weighted floats (below 2^16, exact).
+//
+// A group with no scale, one whose reciprocal FP32 cannot hold, infinities or NaN:
+// the definition's steps as they stand. Not inlined: the eight row pairs of a warp
+// are straight-line code, and every warp passes through all of it.
 template <bool HALF>
+__device__ __noinline__ uint32_t odd_group(uint4 v, float sc, float lo, float& z, bool zeros) {
+    const float d = sc > 0.f ? sc : 1.f;
+    if (zeros) z = fminf(fmaxf(rintf(lo / d), 0.f), 15.f);
+    const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+    uint32_t q[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+        const float f = to_float<HALF>(uint16_t(u[e >> 1] >> (16 * (e & 1))));
+        q[e] = uint32_t(fminf(fmaxf(rintf(f / d) + z, 0.f), 15.f));
+    }
+    return pack8(q);
+}
+
+template <bool HALF, bool ZEROS, int PER>
 __global__ void __launch_bounds__(kQ4Threads)
     q4_quantize_kernel(const uint16_t* __restrict__ w, uint64_t ld, Q4Layout L, uint32_t vec,
                        uint8_t* __restrict__ out) {
     extern __shared__ __align__(16) uint8_t sm[];
+    constexpr int kLanes = 16 / PER;  // of a group
+    constexpr float kSteps = ZEROS ? 15.f : 7.f, kInv = 1.f / kSteps;
     const uint32_t lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const uint32_t b0 = blockIdx.y * 8, s = blockIdx.x;
     const uint32_t h = min(8u, L.blocks16 - b0);
-    const uint32_t lanes = L.group / 8;  // of a group
-    const float steps = L.zeros ? 15.f : 7.f;
     store_header(L, out);
     if (warp < h) {
         uint8_t* rec = sm + warp * L.rec;
         const uint32_t c8 = lane & 15u, c = s * kQ4Cols + 8 * c8;
+        const uint32_t row0 = (b0 + warp) * kQ4Rows + (lane >> 4);
+        const uint16_t* p = w + uint64_t(row0) * ld;
         uint4 v[8];
+        if (vec == 16 && c + 8 <= L.cols) {
 #pragma unroll
-        for (uint32_t k = 0; k < 8; ++k) {
-            const uint32_t row = (b0 + warp) * kQ4Rows + 2 * k + (lane >> 4);
-            v[k] = load8(w + uint64_t(row) * ld, c, L.cols, row < L.rows, vec);
+            for (uint32_t k = 0; k < 8; ++k)
+                v[k] = row0 + 2 * k < L.rows ? ld_stream_v4(p + uint64_t(2 * k) * ld + c)
+                                             : make_uint4(0, 0, 0, 0);
+        } else {
+#pragma unroll
+            for (uint32_t k = 0; k < 8; ++k)
+                v[k] = load8(p + uint64_t(2 * k) * ld, c, L.cols, row0 + 2 * k < L.rows, vec);
         }
+        const uint32_t at = (c8 & 3u) * 256 + (lane >> 4) * 16 + (c8 >> 2) * 4;
+        const bool first = (c8 & (kLanes - 1)) == 0;  // of its group
+        uint8_t* meta = rec + kQ4Codes + (c8 / kLanes * 16 + (lane >> 4)) * 2;
+        uint8_t* zmeta = rec + kQ4Codes + 32 * PER + c8 / kLanes * 16 + (lane >> 4);
 #pragma unroll
         for (uint32_t k = 0; k < 8; ++k) {
-            const uint32_t r = 2 * k + (lane >> 4);
             const uint32_t u[4] = {v[k].x, v[k].y, v[k].z, v[k].w};
             const uint32_t mx = max2<HALF>(max2<HALF>(u[0], u[1]), max2<HALF>(u[2], u[3]));
             const uint32_t mn = min2<HALF>(min2<HALF>(u[0], u[1]), min2<HALF>(u[2], u[3])) ^
@@ -174,53 +213,55 @@ __global__ void __launch_bounds__(kQ4Threads)
             // {even w, even -w} against {odd w, odd -w}, and 0
             uint32_t m = max2<HALF>(prmt(mx, mn, 0x5410u), prmt(mx, mn, 0x7632u));
             m = max2<HALF>(m, 0u);
-            for (uint32_t o = 1; o < lanes; o *= 2)
+#pragma unroll
+            for (int o = 1; o < kLanes; o *= 2)
                 m = max2<HALF>(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
             const float hi = to_float<HALF>(uint16_t(m)), lo = to_float<HALF>(uint16_t(m >> 16));
             // (a NaN made both NaN; infinities of both signs count as one)
             const float inf = __int_as_float(0x7F800000);
-            float range = L.zeros ? hi + lo : fmaxf(hi, lo);
+            float range = ZEROS ? hi + lo : fmaxf(hi, lo);
             if (hi != hi || (hi == inf && lo == inf)) range = __int_as_float(0x7FC00000);
-            const uint16_t sbits = from_float<HALF>(range / steps);
+            // range / steps, again by a Newton step on the remainder
+            const float t0 = range * kInv;
+            const float t1 = fmaf(fmaf(-t0, kSteps, range), kInv, t0);
+            const uint16_t sbits = from_float<HALF>(range < 3e38f ? t1 : range);
             const float sc = to_float<HALF>(sbits);
             uint32_t word;
             float z = 8.f;
-            if (sc > 1e-30f && sc < 1e30f) {
+            if (__builtin_expect(sc > 1e-30f && sc < 1e30f, 1)) {
                 const float r = approx_rcp(sc);
-                if (L.zeros) z = fminf((quotient(lo, sc, r) + kRound) - kRound, 15.f);
+                if (ZEROS) z = fminf((quotient(lo, sc, r) + kRound) - kRound, 15.f);
                 const float zk = z - kRound, top = 15.f - z;
                 float part[2] = {0.f, 0.f};  // even and odd elements
 #pragma unroll
                 for (int e = 7; e >= 0; --e) {
-                    const float f = to_float<HALF>(uint16_t(u[e >> 1] >> (16 * (e & 1))));
+                    const float f = HALF ? to_float<HALF>(uint16_t(u[e >> 1] >> (16 * (e & 1))))
+                                         : __uint_as_float(e & 1 ? u[e >> 1] & 0xFFFF0000u : u[e >> 1] << 16);
                     // clamped before the rounding: the bounds are integers
                     const float t = fminf(fmaxf(quotient(f, sc, r), -z), top);
                     part[e & 1] = fmaf(part[e & 1], 16.f, (t + kRound) + zk);
                 }
                 word = prmt(__float_as_uint(part[0] + 8388608.f), __float_as_uint(part[1] + 8388608.f),
                             0x5410u);
-            } else {  // no scale, one that 1 / s cannot hold, infinity or NaN: the definition's steps
-                const float d = sc > 0.f ? sc : 1.f;
-                if (L.zeros) z = fminf(fmaxf(rintf(lo / d), 0.f), 15.f);
-                uint32_t q[8];
-#pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    const float f = to_float<HALF>(uint16_t(u[e >> 1] >> (16 * (e & 1))));
-                    q[e] = uint32_t(fminf(fmaxf(rintf(f / d) + z, 0.f), 15.f));
-                }
-                word = pack8(q);
+            } else {
+                word = odd_group<HALF>(v[k], sc, lo, z, ZEROS);
             }
-            const uint32_t i = c8 >> 2, t = c8 & 3u;
-            *reinterpret_cast<uint32_t*>(rec + t * 256 + r * 16 + i * 4) = word;
-            if ((c8 & (L.group / 8 - 1)) == 0) {
-                const uint32_t g = c8 / (L.group / 8);
-                *reinterpret_cast<uint16_t*>(rec + kQ4Codes + (g * 16 + r) * 2) = sbits;
-                if (L.zeros) rec[kQ4Codes + 32 * L.per + g * 16 + r] = uint8_t(z);
+            *reinterpret_cast<uint32_t*>(rec + at + k * 32) = word;
+            if (first) {
+                *reinterpret_cast<uint16_t*>(meta + k * 4) = sbits;
+                if (ZEROS) zmeta[k * 2] = uint8_t(z);
             }
         }
-        if (L.zeros && L.per == 1 && lane < 16) rec[kQ4Codes + 32 + 16 + lane] = 0;  // padding
+        if (ZEROS && PER == 1 && lane < 16) rec[kQ4Codes + 32 + 16 + lane] = 0;  // padding
     }
     store_records(out + q4_record(L, b0, s), sm, h * L.rec);
+}
+
+template <bool HALF, bool ZEROS>
+auto quantize_by_group(uint32_t per) {
+    return per == 1   ? q4_quantize_kernel<HALF, ZEROS, 1>
+           : per == 2 ? q4_quantize_kernel<HALF, ZEROS, 2>
+                      : q4_quantize_kernel<HALF, ZEROS, 4>;
 }
 
 __global__ void __launch_bounds__(kQ4Threads)
@@ -304,12 +345,11 @@ __global__ void __launch_bounds__(kQ4Threads)
                     if (c + e < L.cols) o[e] = f[e];
             }
         } else {
-            uint16_t b[8];
+            uint32_t b[4];
 #pragma unroll
-            for (int e = 0; e < 8; ++e) b[e] = from_float<DT == 1>(f[e]);
+            for (int e = 0; e < 4; ++e) b[e] = pack2<DT == 1>(f[2 * e], f[2 * e + 1]);
             store8(static_cast<uint16_t*>(out) + uint64_t(row) * ld, c, L.cols, vec,
-                   make_uint4(b[0] | uint32_t(b[1]) << 16, b[2] | uint32_t(b[3]) << 16,
-                              b[4] | uint32_t(b[5]) << 16, b[6] | uint32_t(b[7]) << 16));
+                   make_uint4(b[0], b[1], b[2], b[3]));
         }
     }
 }
@@ -333,7 +373,10 @@ cudaError_t launch_q4_quantize(const void* w, uint64_t ld, const Q4Layout& L, ui
         q4_header_kernel<<<1, 32, 0, stream>>>(L, out);
         return cudaGetLastError();
     }
-    const auto kernel = L.half_scales ? q4_quantize_kernel<true> : q4_quantize_kernel<false>;
+    const auto kernel =
+        L.half_scales
+            ? (L.zeros ? quantize_by_group<true, true>(L.per) : quantize_by_group<true, false>(L.per))
+            : (L.zeros ? quantize_by_group<false, true>(L.per) : quantize_by_group<false, false>(L.per));
     kernel<<<q4_grid(L), kQ4Threads, 8 * kMaxRec, stream>>>(static_cast<const uint16_t*>(w), ld, L,
                                                             row_align(w, ld, 2), out);
     return cudaGetLastError();
