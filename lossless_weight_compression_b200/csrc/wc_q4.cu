@@ -36,50 +36,32 @@ __device__ __forceinline__ uint32_t pack2(float a, float b) {
     return d;
 }
 
-// Eight consecutive 16-bit values of a row from column c, zeros past the end.
-// `vec`: bytes that divide the address of every row (2 to 16).
-__device__ __forceinline__ uint4 load8(const uint16_t* row, uint32_t c, uint32_t cols, bool live,
-                                       uint32_t vec) {
-    if (!live || c >= cols) return make_uint4(0, 0, 0, 0);
-    if (vec >= 4 && c + 8 <= cols) {
-        if (vec == 16) return ld_stream_v4(row + c);
-        if (vec == 8) {
-            const uint2 a = __ldcs(reinterpret_cast<const uint2*>(row + c));
-            const uint2 b = __ldcs(reinterpret_cast<const uint2*>(row + c + 4));
-            return make_uint4(a.x, a.y, b.x, b.y);
-        }
-        const uint32_t* p = reinterpret_cast<const uint32_t*>(row + c);
-        return make_uint4(__ldcs(p), __ldcs(p + 1), __ldcs(p + 2), __ldcs(p + 3));
-    }
-    uint32_t v[4] = {0, 0, 0, 0};
+// Eight consecutive 16-bit values of a row from column c, zeros past the end, as
+// vectors V that divide the row's address and its length, so that each is inside
+// or outside.
+template <typename V>
+__device__ __forceinline__ uint4 load8(const uint16_t* row, uint32_t c, uint32_t cols, bool live) {
+    constexpr int N = 16 / sizeof(V);
+    V v[N];
 #pragma unroll
-    for (uint32_t k = 0; k < 8; ++k)
-        if (c + k < cols) v[k >> 1] |= uint32_t(row[c + k]) << (16 * (k & 1));
-    return make_uint4(v[0], v[1], v[2], v[3]);
+    for (int k = 0; k < N; ++k) {
+        v[k] = V{};
+        if (live && c + 8 / N * k < cols) v[k] = __ldcs(reinterpret_cast<const V*>(row + c) + k);
+    }
+    uint4 u;
+    memcpy(&u, v, 16);
+    return u;
 }
 
 // Eight 16-bit values to a row from column c, up to the last column.
-__device__ __forceinline__ void store8(uint16_t* row, uint32_t c, uint32_t cols, uint32_t vec,
-                                       uint4 v) {
-    if (vec >= 4 && c + 8 <= cols) {
-        if (vec == 16) {
-            st_stream_v4(row + c, v);
-        } else if (vec == 8) {
-            __stcs(reinterpret_cast<uint2*>(row + c), make_uint2(v.x, v.y));
-            __stcs(reinterpret_cast<uint2*>(row + c + 4), make_uint2(v.z, v.w));
-        } else {
-            uint32_t* p = reinterpret_cast<uint32_t*>(row + c);
-            __stcs(p, v.x);
-            __stcs(p + 1, v.y);
-            __stcs(p + 2, v.z);
-            __stcs(p + 3, v.w);
-        }
-        return;
-    }
-    const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+template <typename V>
+__device__ __forceinline__ void store8(uint16_t* row, uint32_t c, uint32_t cols, uint4 u) {
+    constexpr int N = 16 / sizeof(V);
+    V v[N];
+    memcpy(v, &u, 16);
 #pragma unroll
-    for (uint32_t k = 0; k < 8; ++k)
-        if (c + k < cols) row[c + k] = uint16_t(u[k >> 1] >> (16 * (k & 1)));
+    for (int k = 0; k < N; ++k)
+        if (c + 8 / N * k < cols) __stcs(reinterpret_cast<V*>(row + c) + k, v[k]);
 }
 
 // Adding and subtracting 1.5 * 2^23 rounds |x| < 2^22 to the nearest integer,
@@ -156,8 +138,8 @@ __device__ __forceinline__ void store_header(const Q4Layout& L, uint8_t* out) {
 // floats a lane, max(w, 0) and max(-w, 0); the codes of four elements add up as
 // 16^k-weighted floats (below 2^16, exact).
 //
-// A group with no scale, one whose reciprocal FP32 cannot hold, infinities or NaN:
-// the definition's steps as they stand. Not inlined: the eight row pairs of a warp
+// A scale whose reciprocal FP32 cannot hold, infinities or NaN: the definition's
+// steps as they stand. Not inlined: the eight row pairs of a warp
 // are straight-line code, and every warp passes through all of it.
 template <bool HALF>
 __device__ __noinline__ uint32_t odd_group(uint4 v, float sc, float lo, float& z, bool zeros) {
@@ -190,16 +172,20 @@ __global__ void __launch_bounds__(kQ4Threads)
         const uint32_t row0 = (b0 + warp) * kQ4Rows + (lane >> 4);
         const uint16_t* p = w + uint64_t(row0) * ld;
         uint4 v[8];
-        if (vec == 16 && c + 8 <= L.cols) {
+        auto load = [&](auto vector) {
 #pragma unroll
             for (uint32_t k = 0; k < 8; ++k)
-                v[k] = row0 + 2 * k < L.rows ? ld_stream_v4(p + uint64_t(2 * k) * ld + c)
-                                             : make_uint4(0, 0, 0, 0);
-        } else {
-#pragma unroll
-            for (uint32_t k = 0; k < 8; ++k)
-                v[k] = load8(p + uint64_t(2 * k) * ld, c, L.cols, row0 + 2 * k < L.rows, vec);
-        }
+                v[k] = load8<decltype(vector)>(p + uint64_t(2 * k) * ld, c, L.cols,
+                                               row0 + 2 * k < L.rows);
+        };
+        if (vec == 16)
+            load(uint4());
+        else if (vec == 8)
+            load(uint2());
+        else if (vec == 4)
+            load(uint32_t());
+        else
+            load(static_cast<unsigned short>(0));
         const uint32_t at = (c8 & 3u) * 256 + (lane >> 4) * 16 + (c8 >> 2) * 4;
         const bool first = (c8 & (kLanes - 1)) == 0;  // of its group
         uint8_t* meta = rec + kQ4Codes + (c8 / kLanes * 16 + (lane >> 4)) * 2;
@@ -228,7 +214,10 @@ __global__ void __launch_bounds__(kQ4Threads)
             const float sc = to_float<HALF>(sbits);
             uint32_t word;
             float z = 8.f;
-            if (__builtin_expect(sc > 1e-30f && sc < 1e30f, 1)) {
+            if (sc == 0.f) {  // every code stands for zero
+                z = ZEROS ? 0.f : 8.f;
+                word = ZEROS ? 0u : 0x88888888u;
+            } else if (__builtin_expect(sc > 1e-30f && sc < 1e30f, 1)) {
                 const float r = approx_rcp(sc);
                 if (ZEROS) z = fminf((quotient(lo, sc, r) + kRound) - kRound, 15.f);
                 const float zk = z - kRound, top = 15.f - z;
@@ -348,15 +337,23 @@ __global__ void __launch_bounds__(kQ4Threads)
             uint32_t b[4];
 #pragma unroll
             for (int e = 0; e < 4; ++e) b[e] = pack2<DT == 1>(f[2 * e], f[2 * e + 1]);
-            store8(static_cast<uint16_t*>(out) + uint64_t(row) * ld, c, L.cols, vec,
-                   make_uint4(b[0], b[1], b[2], b[3]));
+            uint16_t* o = static_cast<uint16_t*>(out) + uint64_t(row) * ld;
+            const uint4 u = make_uint4(b[0], b[1], b[2], b[3]);
+            if (vec == 16)
+                store8<uint4>(o, c, L.cols, u);
+            else if (vec == 8)
+                store8<uint2>(o, c, L.cols, u);
+            else if (vec == 4)
+                store8<uint32_t>(o, c, L.cols, u);
+            else
+                store8<unsigned short>(o, c, L.cols, u);
         }
     }
 }
 
-// Bytes (2 to 16) that divide the address of every row.
-uint32_t row_align(const void* p, uint64_t ld, uint32_t size) {
-    const uint64_t a = reinterpret_cast<uintptr_t>(p) | (ld * size);
+// Bytes (2 to 16) that divide the address and the length of every row.
+uint32_t row_align(const void* p, uint64_t ld, uint64_t cols, uint32_t size) {
+    const uint64_t a = reinterpret_cast<uintptr_t>(p) | (ld * size) | (cols * size);
     return a % 16 == 0 ? 16u : a % 8 == 0 ? 8u : a % 4 == 0 ? 4u : 2u;
 }
 
@@ -378,7 +375,7 @@ cudaError_t launch_q4_quantize(const void* w, uint64_t ld, const Q4Layout& L, ui
             ? (L.zeros ? quantize_by_group<true, true>(L.per) : quantize_by_group<true, false>(L.per))
             : (L.zeros ? quantize_by_group<false, true>(L.per) : quantize_by_group<false, false>(L.per));
     kernel<<<q4_grid(L), kQ4Threads, 8 * kMaxRec, stream>>>(static_cast<const uint16_t*>(w), ld, L,
-                                                            row_align(w, ld, 2), out);
+                                                            row_align(w, ld, L.cols, 2), out);
     return cudaGetLastError();
 }
 
@@ -400,7 +397,7 @@ cudaError_t launch_q4_dequantize(const uint8_t* in, const Q4Layout& L, void* out
                         : dtype == 1 ? q4_dequantize_kernel<1>
                                      : q4_dequantize_kernel<0>;
     kernel<<<q4_grid(L), kQ4Threads, 8 * kMaxRec, stream>>>(in, L, out, ld,
-                                                            row_align(out, ld, dtype == 2 ? 4 : 2), status);
+                                                            row_align(out, ld, L.cols, dtype == 2 ? 4 : 2), status);
     return cudaGetLastError();
 }
 
