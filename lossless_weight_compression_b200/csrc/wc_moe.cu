@@ -19,9 +19,9 @@ namespace cg = cooperative_groups;
 // expert found by a ballot per bit of the id, so no atomics); the histograms are
 // scanned over the block's
 // warps, the cluster's blocks (through distributed shared memory) and the
-// experts; then each warp walks its slots again. No workspace and one launch;
-// the ids are read twice, the second time from L2. A few hundred thousand slots
-// take microseconds, far below the row copies that follow.
+// experts; then each warp adds the sums to its slots' ranks. No workspace and one
+// launch. The counting is bound by instruction issue on the cluster's eight
+// multiprocessors (98,304 slots: MEASURED), far below the row copies that follow.
 // ---------------------------------------------------------------------------
 constexpr int kSortThreads = 1024;
 constexpr int kSortWarps = kSortThreads / 32;
@@ -42,7 +42,7 @@ constexpr int kSortBatch = 8;  // ids of a lane loaded ahead of the dependent co
 __global__ void __launch_bounds__(kSortThreads)
     moe_sort_kernel(const int32_t* __restrict__ ids, uint32_t slots, uint32_t experts,
                     int32_t* __restrict__ offsets, int32_t* __restrict__ order,
-                    int32_t* __restrict__ inverse) {
+                    int32_t* inverse) {
     extern __shared__ uint32_t sm[];
     uint32_t* hist = sm;                            // [warps][experts]
     uint32_t* total = sm + kSortWarps * experts;    // [experts] of this block
@@ -69,8 +69,13 @@ __global__ void __launch_bounds__(kSortThreads)
                                              : experts;
 #pragma unroll
         for (int k = 0; k < kSortBatch; ++k) {
+            const uint32_t s = s0 + 32 * k + lane;
             if (s0 + 32 * k >= end) break;
             const uint32_t same = same_id(id[k], bits);
+            // the slot's rank among the warp's of its expert waits in `inverse`
+            if (s < end)
+                inverse[s] = id[k] < experts ? int32_t(mine[id[k]] + __popc(same & below)) : -1;
+            __syncwarp();
             if (id[k] < experts && (same & below) == 0) mine[id[k]] += __popc(same);
             __syncwarp();
         }
@@ -115,29 +120,24 @@ __global__ void __launch_bounds__(kSortThreads)
     uint32_t rows = 0;
     for (int w = 0; w < kSortWarps; ++w) rows += warp_sum[w];
     __syncthreads();
-    for (uint32_t s0 = begin; s0 < end; s0 += 32 * kSortBatch) {
-        uint32_t id[kSortBatch];
+    for (uint32_t s0 = begin + lane; s0 < end; s0 += 32 * kSortBatch) {
+        int32_t id[kSortBatch], pos[kSortBatch];
 #pragma unroll
         for (int k = 0; k < kSortBatch; ++k)
-            id[k] = s0 + 32 * k + lane < end ? min(uint32_t(ids[s0 + 32 * k + lane]), experts)
-                                             : experts;
+            if (s0 + 32 * k < end) {
+                id[k] = ids[s0 + 32 * k];
+                pos[k] = inverse[s0 + 32 * k];  // written by this thread
+            }
 #pragma unroll
         for (int k = 0; k < kSortBatch; ++k) {
-            const uint32_t s = s0 + 32 * k + lane;
-            if (s0 + 32 * k >= end) break;
-            const uint32_t same = same_id(id[k], bits);
-            int32_t pos = -1;
-            if (id[k] < experts) pos = int32_t(base[id[k]] + mine[id[k]] + __popc(same & below));
-            __syncwarp();
-            if (id[k] < experts && (same & below) == 0) mine[id[k]] += __popc(same);
-            __syncwarp();
-            if (s < end) {
-                inverse[s] = pos;
-                if (order != nullptr) {
-                    if (pos >= 0) order[pos] = int32_t(s);
-                    if (s >= rows) order[s] = -1;
-                }
+            const uint32_t s = s0 + 32 * k;
+            if (s >= end) break;
+            if (pos[k] >= 0) {
+                pos[k] += int32_t(base[id[k]] + mine[id[k]]);
+                inverse[s] = pos[k];
+                if (order != nullptr) order[pos[k]] = int32_t(s);
             }
+            if (order != nullptr && s >= rows) order[s] = -1;
         }
     }
 }
@@ -228,12 +228,11 @@ __global__ void __launch_bounds__(kRowThreads)
     }
 }
 
-// Slots are taken kAhead at a time, their rows' vectors all on their way before
-// the first is used (a slot without a row loads nothing and adds nothing): one
-// slot after the other left the memory waiting for indices (186 -> MEASURED).
-constexpr int kAhead = 4;
-
-template <typename T, typename V, int UNROLL>
+// Slots are taken AHEAD at a time, UNROLL vectors a lane of each, all on their way
+// before the first is used (a slot without a row loads nothing and adds nothing):
+// one slot after the other left the memory waiting for indices (16,384 tokens of
+// 6 rows of 4 KB: 186 us, so 75, where the bytes take 67).
+template <typename T, typename V, int AHEAD, int UNROLL>
 __global__ void __launch_bounds__(kRowThreads)
     moe_combine_kernel(RowParams P, const uint8_t* __restrict__ y, uint64_t ldy,
                        const float* __restrict__ weights, uint8_t* __restrict__ out, uint64_t ldo) {
@@ -244,24 +243,24 @@ __global__ void __launch_bounds__(kRowThreads)
     if (tok >= P.tokens) return;
     const uint32_t v0 = uint32_t(unit % P.segs) * (32 * UNROLL) + lane;
     float acc[UNROLL][N] = {};
-    for (uint32_t j0 = 0; j0 < P.top; j0 += kAhead) {
-        int32_t p[kAhead];
-        float w[kAhead];
+    for (uint32_t j0 = 0; j0 < P.top; j0 += AHEAD) {
+        int32_t p[AHEAD];
+        float w[AHEAD];
 #pragma unroll
-        for (int j = 0; j < kAhead; ++j) {
+        for (int j = 0; j < AHEAD; ++j) {
             p[j] = j0 + j < P.top ? P.inverse[tok * P.top + j0 + j] : -1;
             if (p[j] >= 0 && uint64_t(p[j]) >= P.rows) p[j] = -1;
             w[j] = weights != nullptr && p[j] >= 0 ? weights[tok * P.top + j0 + j] : 1.f;
         }
-        V v[kAhead][UNROLL];
+        V v[AHEAD][UNROLL];
 #pragma unroll
-        for (int j = 0; j < kAhead; ++j)
+        for (int j = 0; j < AHEAD; ++j)
 #pragma unroll
             for (int k = 0; k < UNROLL; ++k)
                 if (p[j] >= 0 && v0 + 32 * k < P.nvec)
                     v[j][k] = ldg_stream(reinterpret_cast<const V*>(y + uint64_t(p[j]) * ldy) + v0 + 32 * k);
 #pragma unroll
-        for (int j = 0; j < kAhead; ++j) {
+        for (int j = 0; j < AHEAD; ++j) {
             if (p[j] < 0) continue;
 #pragma unroll
             for (int k = 0; k < UNROLL; ++k)
@@ -282,28 +281,27 @@ __global__ void __launch_bounds__(kRowThreads)
 // dy[p] = w * dout[token] and dw = <dout[token], y[p]> of each slot: P.team
 // threads (32 to 256) own a token, so that dout is read once and each product's
 // sum stays in registers until one reduction in a fixed order. Slots are taken
-// kBwSlots at a time, with two vectors of each on their way.
-constexpr int kBwSlots = 4;
+// SLOTS at a time, with kBwUnroll vectors of each on their way.
 constexpr int kBwUnroll = 2;
 
-template <typename T, typename V>
+template <typename T, typename V, int SLOTS>
 __global__ void __launch_bounds__(kRowThreads)
     moe_combine_backward_kernel(RowParams P, const uint8_t* __restrict__ dout, uint64_t ldd,
                                 const uint8_t* __restrict__ y, uint64_t ldy,
                                 const float* __restrict__ weights, uint8_t* __restrict__ dy,
                                 uint64_t lddy, float* __restrict__ dweights) {
     constexpr int N = sizeof(V) / sizeof(T);
-    __shared__ float red[kBwSlots][kRowThreads / 32];
+    __shared__ float red[SLOTS][kRowThreads / 32];
     const uint32_t lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const uint32_t tid = threadIdx.x % P.team;
     const uint64_t tok = uint64_t(blockIdx.x) * (kRowThreads / P.team) + threadIdx.x / P.team;
     const bool live = tok < P.tokens;  // (every thread reaches the barriers)
     const V* d = reinterpret_cast<const V*>(dout + tok * ldd);
-    for (uint32_t j0 = 0; j0 < P.top; j0 += kBwSlots) {
-        int32_t p[kBwSlots];
-        float w[kBwSlots], dot[kBwSlots];
+    for (uint32_t j0 = 0; j0 < P.top; j0 += SLOTS) {
+        int32_t p[SLOTS];
+        float w[SLOTS], dot[SLOTS];
 #pragma unroll
-        for (int j = 0; j < kBwSlots; ++j) {
+        for (int j = 0; j < SLOTS; ++j) {
             dot[j] = 0.f;
             w[j] = 1.f;
             p[j] = -1;
@@ -315,14 +313,14 @@ __global__ void __launch_bounds__(kRowThreads)
         }
         if (live) {
             for (uint32_t v0 = tid; v0 < P.nvec; v0 += kBwUnroll * P.team) {
-                V dv[kBwUnroll], yv[kBwSlots][kBwUnroll];
+                V dv[kBwUnroll], yv[SLOTS][kBwUnroll];
 #pragma unroll
                 for (int k = 0; k < kBwUnroll; ++k) {
                     const uint32_t v = v0 + k * P.team;
                     if (v >= P.nvec) continue;
                     dv[k] = d[v];
 #pragma unroll
-                    for (int j = 0; j < kBwSlots; ++j)
+                    for (int j = 0; j < SLOTS; ++j)
                         if (p[j] >= 0)
                             yv[j][k] = ldg_stream(reinterpret_cast<const V*>(y + uint64_t(p[j]) * ldy) + v);
                 }
@@ -333,7 +331,7 @@ __global__ void __launch_bounds__(kRowThreads)
                     float df[N];
                     unpack<T, V>(dv[k], df);
 #pragma unroll
-                    for (int j = 0; j < kBwSlots; ++j) {
+                    for (int j = 0; j < SLOTS; ++j) {
                         if (p[j] < 0) continue;
                         float f[N];
                         unpack<T, V>(yv[j][k], f);
@@ -349,13 +347,13 @@ __global__ void __launch_bounds__(kRowThreads)
         }
         if (dweights != nullptr) {
 #pragma unroll
-            for (int j = 0; j < kBwSlots; ++j) {
+            for (int j = 0; j < SLOTS; ++j) {
 #pragma unroll
                 for (int o = 16; o > 0; o /= 2) dot[j] += __shfl_xor_sync(0xFFFFFFFFu, dot[j], o);
                 if (lane == 0) red[j][warp] = dot[j];
             }
             __syncthreads();
-            if (live && tid < kBwSlots && j0 + tid < P.top) {
+            if (live && tid < SLOTS && j0 + tid < P.top) {
                 const uint32_t w0 = threadIdx.x / P.team * (P.team / 32);
                 float sum = 0.f;
                 for (uint32_t k = 0; k < P.team / 32; ++k) sum += red[tid][w0 + k];
@@ -475,16 +473,19 @@ cudaError_t launch_moe_combine(const MoeArgs& a, const void* y, uint64_t ldy, co
     const uint32_t v = vec_bytes(reinterpret_cast<uintptr_t>(y) | (ldy * es) |
                                      reinterpret_cast<uintptr_t>(out) | (ldo * es) | (a.cols * es),
                                  es);
-    // Two vectors a lane where a row is long enough to fill the machine so, one
-    // where there are few rows.
+    // Eight vectors a lane on their way where there are rows enough to fill the
+    // machine so, as the slots have it; one of each slot where there are few.
     const uint64_t vectors = a.tokens * (a.cols * es / v);
-    const int unroll = vectors >= (1u << 19) ? 2 : 1;
+    const int unroll = vectors < (1u << 19) ? 1 : a.top <= 2 ? 4 : 2;
     const RowParams P = row_params(a, v, unroll);
     const uint64_t blocks = (a.tokens * P.segs * 32 + kRowThreads - 1) / kRowThreads;
     if (blocks > 0x7FFFFFFFull) return too_large();
     return by_type(a.dtype, v, [&](auto t, auto vec) {
-        const auto kernel = unroll == 2 ? moe_combine_kernel<decltype(t), decltype(vec), 2>
-                                        : moe_combine_kernel<decltype(t), decltype(vec), 1>;
+        using T = decltype(t);
+        using V = decltype(vec);
+        const auto kernel = unroll == 4   ? moe_combine_kernel<T, V, 2, 4>
+                            : unroll == 2 ? moe_combine_kernel<T, V, 4, 2>
+                                          : moe_combine_kernel<T, V, 4, 1>;
         kernel<<<uint32_t(blocks), kRowThreads, 0, stream>>>(P, static_cast<const uint8_t*>(y),
                                                              ldy * es, weights,
                                                              static_cast<uint8_t*>(out), ldo * es);
@@ -508,10 +509,13 @@ cudaError_t launch_moe_combine_backward(const MoeArgs& a, const void* dout, uint
     const uint64_t blocks = (a.tokens + per - 1) / per;
     if (blocks > 0x7FFFFFFFull) return too_large();
     return by_type(a.dtype, v, [&](auto t, auto vec) {
-        moe_combine_backward_kernel<decltype(t), decltype(vec)>
-            <<<uint32_t(blocks), kRowThreads, 0, stream>>>(
-                P, static_cast<const uint8_t*>(dout), ldd * es, static_cast<const uint8_t*>(y),
-                ldy * es, weights, static_cast<uint8_t*>(dy), lddy * es, dweights);
+        using T = decltype(t);
+        using V = decltype(vec);
+        const auto kernel = a.top <= 2 ? moe_combine_backward_kernel<T, V, 2>
+                                       : moe_combine_backward_kernel<T, V, 4>;
+        kernel<<<uint32_t(blocks), kRowThreads, 0, stream>>>(
+            P, static_cast<const uint8_t*>(dout), ldd * es, static_cast<const uint8_t*>(y), ldy * es,
+            weights, static_cast<uint8_t*>(dy), lddy * es, dweights);
         return cudaGetLastError();
     });
 }
