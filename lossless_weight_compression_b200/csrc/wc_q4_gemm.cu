@@ -11,13 +11,13 @@
 //     loads the slice's activations by TMA in the 128-byte swizzled K-major
 //     layout the MMA reads B in (two warps with narrower copies when the rows
 //     of x are not 16-byte aligned);
-//   - twelve unpacking warps, four per slice in turns, one lane per row, turn
+//   - eight unpacking warps, four per slice in turns, one lane per row, turn
 //     codes into 16-bit integers q - z and store them as the A operand into
 //     tensor memory;
 //   - two warps issue tcgen05.mma, each GROUP of columns into an accumulator
 //     of its own in tensor memory: the products are exact and a group sums at
 //     most 128 of them;
-//   - eight scaling warps read a group's accumulator (tcgen05.ld), scale it in
+//   - sixteen scaling warps read a group's accumulator (tcgen05.ld), scale it in
 //     FP32 and add it to the row's sums in registers.
 // Scaling sums instead of weights keeps every weight exact (s (q - z) has up to
 // 15 significant bits, a BF16 operand 8) and bounds the unspecified rounding of
@@ -49,17 +49,20 @@ constexpr uint32_t kSmemMax = 232448;
 
 constexpr int kMWarps = 2;
 constexpr int kWWarp = 0, kMWarp0 = 2;  // 1: activations; 2, 3: MMA issue
-constexpr int kUnpWarp0 = 4;    // 4..15: lane quarter warp % 4, slices in turns of three
-constexpr int kUnpTurns = 3;
-constexpr int kSclWarp0 = 16;   // 16..23: lane quarter warp % 4, half of the columns
-constexpr int kSclWarps = 8;
-constexpr int kQ4GemmThreads = 32 * 24;
+constexpr int kUnpTurns = 2;
+constexpr int kUnpWarp0 = 4;    // 4..11: lane quarter warp % 4, slices in turns
+constexpr int kSclWarp0 = kUnpWarp0 + 4 * kUnpTurns;  // 12..27: lane quarter warp % 4, columns
+constexpr int kSclWarps = 16;
+constexpr int kGemmWarps = kSclWarp0 + kSclWarps;
+constexpr int kQ4GemmThreads = 32 * kGemmWarps;
 
-// Registers of a thread after the roles split (of 80 at launch: (4 + 12) x 48 +
-// 8 x 144 warps = 24 x 80): a scaling warp holds up to 64 sums and as many
-// results on their way.
-constexpr int kRegsLaunch = 80, kRegsIssue = 48, kRegsUnpack = 48, kRegsScale = 144;
-static_assert(4 * kRegsIssue + 12 * kRegsUnpack + 8 * kRegsScale == 24 * kRegsLaunch, "registers");
+// Registers of a thread after the roles split: a scaling warp holds up to 32
+// sums and as many results on their way.
+constexpr int kRegsLaunch = 72, kRegsIssue = 48, kRegsUnpack = 48, kRegsScale = 88;
+static_assert(kQ4GemmThreads * kRegsLaunch <= 65536, "registers at launch");
+static_assert(4 * kRegsIssue + 4 * kUnpTurns * kRegsUnpack + kSclWarps * kRegsScale <=
+                  kGemmWarps * kRegsLaunch,
+              "the roles' registers come out of those at launch");
 
 // Accumulators of NT columns: group number n of the block goes to n % accs.
 template <int NT, int PER>
@@ -516,58 +519,95 @@ __device__ __forceinline__ void store_y(const GmParams& P, uint64_t tok, uint32_
         static_cast<float*>(P.a.y)[tok * P.a.ldy + row] = v;
 }
 
-// HN consecutive FP32 columns of this thread's tensor memory lane.
-__device__ __forceinline__ void tmem_ld_cols(uint32_t a, uint32_t (&v)[16]) { tmem_ld16(a, v); }
-__device__ __forceinline__ void tmem_ld_cols(uint32_t a, uint32_t (&v)[32]) {
+// A group's results (consecutive FP32 columns of this thread's tensor memory
+// lane) scaled and added to the sums, two a instruction, each FMA rounded to
+// nearest; once they are read, one lane says so on `bar`. One block of assembly,
+// so that the pairs stay where tcgen05.ld put them (through C++ values each
+// pair was moved first).
+__device__ __forceinline__ void scale_add(uint64_t (&sum)[16], uint32_t taddr, uint32_t bar,
+                                          uint32_t arrive, uint64_t s2) {
     asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,"
-        "%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
-        : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]),
-          "=r"(v[7]), "=r"(v[8]), "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]),
-          "=r"(v[14]), "=r"(v[15]), "=r"(v[16]), "=r"(v[17]), "=r"(v[18]), "=r"(v[19]),
-          "=r"(v[20]), "=r"(v[21]), "=r"(v[22]), "=r"(v[23]), "=r"(v[24]), "=r"(v[25]),
-          "=r"(v[26]), "=r"(v[27]), "=r"(v[28]), "=r"(v[29]), "=r"(v[30]), "=r"(v[31])
-        : "r"(a));
-    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
-}
-// (two loads: one of 64 registers does not fit those of a thread at launch)
-__device__ __forceinline__ void tmem_ld_cols(uint32_t a, uint32_t (&v)[64]) {
-    asm volatile(
+        "{\n\t.reg .b32 v<32>;\n\t.reg .b64 p;\n\t.reg .pred f;\n\t"
         "tcgen05.ld.sync.aligned.32x32b.x32.b32 {"
-        "%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,"
-        "%25,%26,%27,%28,%29,%30,%31"
-        "}, [%64];\n\t"
-        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {"
-        "%32,%33,%34,%35,%36,%37,%38,%39,%40,%41,%42,%43,%44,%45,%46,%47,%48,%49,%50,%51,%52,%53,"
-        "%54,%55,%56,%57,%58,%59,%60,%61,%62,%63"
-        "}, [%65];\n\t"
-        "tcgen05.wait::ld.sync.aligned;"
-        : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]),
-          "=r"(v[5]), "=r"(v[6]), "=r"(v[7]), "=r"(v[8]), "=r"(v[9]),
-          "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]),
-          "=r"(v[15]), "=r"(v[16]), "=r"(v[17]), "=r"(v[18]), "=r"(v[19]),
-          "=r"(v[20]), "=r"(v[21]), "=r"(v[22]), "=r"(v[23]), "=r"(v[24]),
-          "=r"(v[25]), "=r"(v[26]), "=r"(v[27]), "=r"(v[28]), "=r"(v[29]),
-          "=r"(v[30]), "=r"(v[31]), "=r"(v[32]), "=r"(v[33]), "=r"(v[34]),
-          "=r"(v[35]), "=r"(v[36]), "=r"(v[37]), "=r"(v[38]), "=r"(v[39]),
-          "=r"(v[40]), "=r"(v[41]), "=r"(v[42]), "=r"(v[43]), "=r"(v[44]),
-          "=r"(v[45]), "=r"(v[46]), "=r"(v[47]), "=r"(v[48]), "=r"(v[49]),
-          "=r"(v[50]), "=r"(v[51]), "=r"(v[52]), "=r"(v[53]), "=r"(v[54]),
-          "=r"(v[55]), "=r"(v[56]), "=r"(v[57]), "=r"(v[58]), "=r"(v[59]),
-          "=r"(v[60]), "=r"(v[61]), "=r"(v[62]), "=r"(v[63])
-        : "r"(a), "r"(a + 32u)
+        "v0,v1,v2,v3,v4,v5,v6,v7,v8,v9,v10,v11,v12,v13,v14,v15,v16,v17,v18,v19,v20,"
+        "v21,v22,v23,v24,v25,v26,v27,v28,v29,v30,v31}, [%16];\n\t"
+        "tcgen05.wait::ld.sync.aligned;\n\t"
+        "tcgen05.fence::before_thread_sync;\n\t"
+        "bar.warp.sync 0xFFFFFFFF;\n\t"
+        "setp.ne.u32 f, %18, 0;\n\t"
+        "@f mbarrier.arrive.shared::cta.b64 _, [%17];\n\t"
+        "mov.b64 p, {v0, v1};\n\tfma.rn.f32x2 %0, %19, p, %0;\n\t"
+        "mov.b64 p, {v2, v3};\n\tfma.rn.f32x2 %1, %19, p, %1;\n\t"
+        "mov.b64 p, {v4, v5};\n\tfma.rn.f32x2 %2, %19, p, %2;\n\t"
+        "mov.b64 p, {v6, v7};\n\tfma.rn.f32x2 %3, %19, p, %3;\n\t"
+        "mov.b64 p, {v8, v9};\n\tfma.rn.f32x2 %4, %19, p, %4;\n\t"
+        "mov.b64 p, {v10, v11};\n\tfma.rn.f32x2 %5, %19, p, %5;\n\t"
+        "mov.b64 p, {v12, v13};\n\tfma.rn.f32x2 %6, %19, p, %6;\n\t"
+        "mov.b64 p, {v14, v15};\n\tfma.rn.f32x2 %7, %19, p, %7;\n\t"
+        "mov.b64 p, {v16, v17};\n\tfma.rn.f32x2 %8, %19, p, %8;\n\t"
+        "mov.b64 p, {v18, v19};\n\tfma.rn.f32x2 %9, %19, p, %9;\n\t"
+        "mov.b64 p, {v20, v21};\n\tfma.rn.f32x2 %10, %19, p, %10;\n\t"
+        "mov.b64 p, {v22, v23};\n\tfma.rn.f32x2 %11, %19, p, %11;\n\t"
+        "mov.b64 p, {v24, v25};\n\tfma.rn.f32x2 %12, %19, p, %12;\n\t"
+        "mov.b64 p, {v26, v27};\n\tfma.rn.f32x2 %13, %19, p, %13;\n\t"
+        "mov.b64 p, {v28, v29};\n\tfma.rn.f32x2 %14, %19, p, %14;\n\t"
+        "mov.b64 p, {v30, v31};\n\tfma.rn.f32x2 %15, %19, p, %15;\n\t"
+        "}"
+        : "+l"(sum[0]), "+l"(sum[1]), "+l"(sum[2]), "+l"(sum[3]), "+l"(sum[4]),
+          "+l"(sum[5]), "+l"(sum[6]), "+l"(sum[7]), "+l"(sum[8]), "+l"(sum[9]),
+          "+l"(sum[10]), "+l"(sum[11]), "+l"(sum[12]), "+l"(sum[13]), "+l"(sum[14]),
+          "+l"(sum[15])
+        : "r"(taddr), "r"(bar), "r"(arrive), "l"(s2)
         : "memory");
 }
 
-// Two FP32 FMAs in one instruction, each rounded to nearest; the sums stay
-// register pairs.
-__device__ __forceinline__ void fma2(uint64_t& acc, uint64_t s2, uint32_t v0, uint32_t v1) {
-    asm("{\n\t.reg .b64 b;\n\t"
-        "mov.b64 b, {%2, %3};\n\t"
-        "fma.rn.f32x2 %0, %1, b, %0;\n\t}"
-        : "+l"(acc)
-        : "l"(s2), "r"(v0), "r"(v1));
+__device__ __forceinline__ void scale_add(uint64_t (&sum)[8], uint32_t taddr, uint32_t bar,
+                                          uint32_t arrive, uint64_t s2) {
+    asm volatile(
+        "{\n\t.reg .b32 v<16>;\n\t.reg .b64 p;\n\t.reg .pred f;\n\t"
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {"
+        "v0,v1,v2,v3,v4,v5,v6,v7,v8,v9,v10,v11,v12,v13,v14,v15}, [%8];\n\t"
+        "tcgen05.wait::ld.sync.aligned;\n\t"
+        "tcgen05.fence::before_thread_sync;\n\t"
+        "bar.warp.sync 0xFFFFFFFF;\n\t"
+        "setp.ne.u32 f, %10, 0;\n\t"
+        "@f mbarrier.arrive.shared::cta.b64 _, [%9];\n\t"
+        "mov.b64 p, {v0, v1};\n\tfma.rn.f32x2 %0, %11, p, %0;\n\t"
+        "mov.b64 p, {v2, v3};\n\tfma.rn.f32x2 %1, %11, p, %1;\n\t"
+        "mov.b64 p, {v4, v5};\n\tfma.rn.f32x2 %2, %11, p, %2;\n\t"
+        "mov.b64 p, {v6, v7};\n\tfma.rn.f32x2 %3, %11, p, %3;\n\t"
+        "mov.b64 p, {v8, v9};\n\tfma.rn.f32x2 %4, %11, p, %4;\n\t"
+        "mov.b64 p, {v10, v11};\n\tfma.rn.f32x2 %5, %11, p, %5;\n\t"
+        "mov.b64 p, {v12, v13};\n\tfma.rn.f32x2 %6, %11, p, %6;\n\t"
+        "mov.b64 p, {v14, v15};\n\tfma.rn.f32x2 %7, %11, p, %7;\n\t"
+        "}"
+        : "+l"(sum[0]), "+l"(sum[1]), "+l"(sum[2]), "+l"(sum[3]), "+l"(sum[4]),
+          "+l"(sum[5]), "+l"(sum[6]), "+l"(sum[7])
+        : "r"(taddr), "r"(bar), "r"(arrive), "l"(s2)
+        : "memory");
 }
+
+__device__ __forceinline__ void scale_add(uint64_t (&sum)[4], uint32_t taddr, uint32_t bar,
+                                          uint32_t arrive, uint64_t s2) {
+    asm volatile(
+        "{\n\t.reg .b32 v<8>;\n\t.reg .b64 p;\n\t.reg .pred f;\n\t"
+        "tcgen05.ld.sync.aligned.32x32b.x8.b32 {"
+        "v0,v1,v2,v3,v4,v5,v6,v7}, [%4];\n\t"
+        "tcgen05.wait::ld.sync.aligned;\n\t"
+        "tcgen05.fence::before_thread_sync;\n\t"
+        "bar.warp.sync 0xFFFFFFFF;\n\t"
+        "setp.ne.u32 f, %6, 0;\n\t"
+        "@f mbarrier.arrive.shared::cta.b64 _, [%5];\n\t"
+        "mov.b64 p, {v0, v1};\n\tfma.rn.f32x2 %0, %7, p, %0;\n\t"
+        "mov.b64 p, {v2, v3};\n\tfma.rn.f32x2 %1, %7, p, %1;\n\t"
+        "mov.b64 p, {v4, v5};\n\tfma.rn.f32x2 %2, %7, p, %2;\n\t"
+        "mov.b64 p, {v6, v7};\n\tfma.rn.f32x2 %3, %7, p, %3;\n\t"
+        "}"
+        : "+l"(sum[0]), "+l"(sum[1]), "+l"(sum[2]), "+l"(sum[3])
+        : "r"(taddr), "r"(bar), "r"(arrive), "l"(s2)
+        : "memory");
+}
+
 __device__ __forceinline__ uint64_t pair2(float s) {
     uint64_t d;
     asm("mov.b64 %0, {%1, %1};" : "=l"(d) : "f"(s));
@@ -582,12 +622,12 @@ __device__ void gm_scale(const GmParams& P, const GmSmem& S, int wi, int lane) {
     GmCtl& c = *S.ctl;
     const Q4Layout& L = P.L;
     constexpr uint32_t ACCS = accs<NT, PER>();
-    constexpr int HN = NT / 2;  // columns of this warp
-    const uint32_t q = uint32_t(wi) & 3u, half = uint32_t(wi) >> 2;
+    constexpr int HN = NT / (kSclWarps / 4);  // columns of this warp
+    const uint32_t q = uint32_t(wi) & 3u, part = uint32_t(wi) >> 2;
     const uint32_t r = 32u * q + uint32_t(lane);
     const uint32_t scale_at = smem_addr(S.w) + (r >> 4) * L.rec + kQ4Codes + (r & 15u) * 2u;
     const uint32_t half_scales = L.half_scales;
-    const uint32_t t_lane = c.tmem_base + ((32u * q) << 16) + half * HN;
+    const uint32_t t_lane = c.tmem_base + ((32u * q) << 16) + part * HN;
     uint32_t s0, s1, e = 0, count = 0;
     my_slices(P, s0, s1);
     if (lane == 0)  // the first groups' accumulators are free
@@ -599,7 +639,7 @@ __device__ void gm_scale(const GmParams& P, const GmSmem& S, int wi, int lane) {
         uint64_t sum[HN / 2];
 #pragma unroll
         for (int k = 0; k < HN / 2; ++k) sum[k] = 0;  // two FP32 zeros
-        const uint32_t live = t.ntok > half * HN ? t.ntok - half * HN : 0u;  // columns in use
+        const uint32_t live = t.ntok > part * HN ? t.ntok - part * HN : 0u;  // columns in use
         for (const uint32_t end = count + (s1 - s0); count < end; ++count) {
             const uint32_t st = count % kSRing, round = count / kSRing, ws = count % kWRing;
 #pragma unroll
@@ -614,18 +654,16 @@ __device__ void gm_scale(const GmParams& P, const GmSmem& S, int wi, int lane) {
                 asm volatile("ld.shared.u16 %0, [%1];"
                              : "=h"(bits)
                              : "r"(scale_at + ws * kWStage + 32u * g));
-                uint32_t v[HN];
-                if (live > 0) tmem_ld_cols(t_lane + gi % ACCS * NT, v);
-                tc_fence_before();
                 const uint64_t sc = pair2(q4_scale(bits, half_scales));
-                __syncwarp();
-                if (lane == 0) {
-                    mbar_arrive(&c.g_full[next / PER % kSRing][next % PER]);
-                    if (g == PER - 1) mbar_arrive(&c.w_empty[ws]);
-                }
+                unsigned long long* bar = &c.g_full[next / PER % kSRing][next % PER];
                 if (live > 0) {
-#pragma unroll
-                    for (int k = 0; k < HN / 2; ++k) fma2(sum[k], sc, v[2 * k], v[2 * k + 1]);
+                    scale_add(sum, t_lane + gi % ACCS * NT, smem_addr(bar), lane == 0, sc);
+                } else {
+                    if (lane == 0) mbar_arrive(bar);
+                }
+                if (g == PER - 1) {
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&c.w_empty[ws]);
                 }
             }
         }
@@ -635,14 +673,14 @@ __device__ void gm_scale(const GmParams& P, const GmSmem& S, int wi, int lane) {
 #pragma unroll
                 for (int k = 0; k < HN; ++k)
                     if (uint32_t(k) < live)
-                        store_y<HALF>(P, uint64_t(t.tok0) + half * HN + k, row,
+                        store_y<HALF>(P, uint64_t(t.tok0) + part * HN + k, row,
                                       half2f(sum[k / 2], k & 1));
             }
         } else {  // the block's only unit: every copy into the ring has been used
             float* red = reinterpret_cast<float*>(S.x);
 #pragma unroll
             for (int k = 0; k < HN; ++k)
-                red[(half * HN + k) * kRowsTile + r] = half2f(sum[k / 2], k & 1);
+                red[(part * HN + k) * kRowsTile + r] = half2f(sum[k / 2], k & 1);
         }
     }
 }
