@@ -399,7 +399,7 @@ __device__ void gm_unpack(const GmParams& P, const GmSmem& S, int wi, int lane) 
     const uint32_t r = 32u * q + uint32_t(lane);
     const uint32_t row_at = smem_addr(S.w) + (r >> 4) * L.rec + (r & 15u) * 16u;
     const uint32_t zero_at = smem_addr(S.w) + (r >> 4) * L.rec + kQ4Codes + 32u * PER + (r & 15u);
-    const uint32_t t_lane = c.tmem_base + ((32u * q) << 16) + kACol;
+    const uint32_t t_lane = ((32u * q) << 16) + kACol;
     const uint32_t total = all_slices<NT>(P, S);
     const bool zeros = L.zeros != 0;
     for (uint32_t n = turn; n < total; n += kUnpTurns) {
@@ -449,10 +449,13 @@ __device__ void gm_unpack(const GmParams& P, const GmSmem& S, int wi, int lane) 
 // wait returns only after the MMAs it issued before have left its queue (a
 // barrier poll or any other read of shared memory behind 8 of them costs some
 // 170 cycles), so there is one wait a group and the other warp's MMAs run
-// meanwhile. The whole warp walks, so that addresses and descriptors stay in
-// uniform registers; one lane issues.
-template <int NT, bool HALF, int PER>
-__device__ void gm_mma(const GmParams& P, const GmSmem& S, uint32_t turn) {
+// meanwhile. The whole warp walks and one lane issues; everything an MMA is
+// given is uniform to the compiler's eye (the warp's number a constant, what
+// comes from shared memory through a vote or a reduction), or each operand is
+// moved from a vector register in a loop of its own: 12 moves an MMA, 430
+// cycles for 4 of them.
+template <int NT, bool HALF, int PER, int TURN>
+__device__ void gm_mma(const GmParams& P, const GmSmem& S) {
     GmCtl& c = *S.ctl;
     constexpr uint32_t ACCS = accs<NT, PER>();
     constexpr int kGroups = PER == 1 ? 1 : PER / 2;  // of this warp in a slice it takes
@@ -463,31 +466,31 @@ __device__ void gm_mma(const GmParams& P, const GmSmem& S, uint32_t turn) {
     bool ok = true, issued = false;
     for (uint32_t u = blockIdx.x / P.split; ok; u += gridDim.x / P.split) {
         const GmUnit t = unit_at<NT>(P, S, u, e);
-        if (!t.valid) break;
+        if (!__any_sync(0xFFFFFFFFu, t.valid)) break;
         e = t.e;
         // kind::f16: FP32 accumulator, A and B both BF16 or both FP16 (0 in bits 7-12)
-        const uint32_t nn = (t.ntok + 15u) & ~15u;
+        const uint32_t nn = __reduce_max_sync(0xFFFFFFFFu, (t.ntok + 15u) & ~15u);
         const uint32_t idesc = HALF ? bf16_idesc(kRowsTile, nn) & ~((1u << 7) | (1u << 10))
                                     : bf16_idesc(kRowsTile, nn);
         const uint32_t end = count + (s1 - s0);
-        for (uint32_t n = PER == 1 ? count + ((count ^ turn) & 1u) : count; ok && n < end;
+        for (uint32_t n = PER == 1 ? count + ((count ^ TURN) & 1u) : count; ok && n < end;
              n += PER == 1 ? kMWarps : 1) {
             const uint32_t st = n % kSRing, round = n / kSRing;
-            const uint32_t ta = c.tmem_base + kACol + st * 64u;
+            const uint32_t ta = kACol + st * 64u;
             const uint64_t xd0 = sw128_desc(x0 + st * (NT * 256));
             const uint64_t xd1 = xd0 + NT * 8;
 #pragma unroll
             for (int j = 0; j < kGroups; ++j) {
-                const uint32_t g = PER == 1 ? 0u : turn * kGroups + j;
+                const uint32_t g = PER == 1 ? 0u : TURN * kGroups + j;
                 if (!gm_wait_warp(&c.g_full[st][g], round & 1u, c, P.a.status)) {
                     ok = false;
                     break;
                 }
                 tc_fence_after();
-                const uint32_t acc = c.tmem_base + (n * PER + g) % ACCS * NT;
+                const uint32_t acc = (n * PER + g) % ACCS * NT;
                 // the group's first K step: 8 columns of A and 32 bytes of B each
                 const uint32_t a0 = ta + 8u * kMmas * g;
-                const uint64_t b0 = PER == 1 ? xd0 : (turn ? xd1 : xd0) + 2u * kMmas * j;
+                const uint64_t b0 = PER == 1 ? xd0 : (TURN ? xd1 : xd0) + 2u * kMmas * j;
                 if (elect_one()) {
 #pragma unroll
                     for (int k = 0; k < kMmas; ++k)
@@ -505,8 +508,8 @@ __device__ void gm_mma(const GmParams& P, const GmSmem& S, uint32_t turn) {
     }
     if (issued) {  // every MMA has finished before the block ends (elect.sync picks one lane
                    // throughout, so the commit covers all of the warp's)
-        if (elect_one()) umma_commit(&c.drain[turn]);
-        mbar_wait(&c.drain[turn], 0, nullptr);
+        if (elect_one()) umma_commit(&c.drain[TURN]);
+        mbar_wait(&c.drain[TURN], 0, nullptr);
     }
 }
 
@@ -627,7 +630,7 @@ __device__ void gm_scale(const GmParams& P, const GmSmem& S, int wi, int lane) {
     const uint32_t r = 32u * q + uint32_t(lane);
     const uint32_t scale_at = smem_addr(S.w) + (r >> 4) * L.rec + kQ4Codes + (r & 15u) * 2u;
     const uint32_t half_scales = L.half_scales;
-    const uint32_t t_lane = c.tmem_base + ((32u * q) << 16) + part * HN;
+    const uint32_t t_lane = ((32u * q) << 16) + part * HN;
     uint32_t s0, s1, e = 0, count = 0;
     my_slices(P, s0, s1);
     if (lane == 0)  // the first groups' accumulators are free
@@ -759,13 +762,22 @@ __global__ void __launch_bounds__(kQ4GemmThreads, 1)
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
+    // All 512 columns are this block's, so its tensor memory starts at address 0,
+    // which the roles use as a constant.
+    if (c.tmem_base != 0) {
+        if (tid == 0) report(P.a.status, kStatusTimeout);
+        c.abort = 1;
+    }
 
     if (warp < kUnpWarp0) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsIssue));
         if (warp == kWWarp) {
             if (lane == 0) gm_load_w<NT>(P, S);
         } else if (warp >= kMWarp0) {
-            gm_mma<NT, HALF, PER>(P, S, warp - kMWarp0);
+            if (warp == kMWarp0)
+                gm_mma<NT, HALF, PER, 0>(P, S);
+            else
+                gm_mma<NT, HALF, PER, 1>(P, S);
         } else if (P.x_bytes == 16) {
             if (lane == 0) gm_load_x_tma<NT, PER>(P, S);
         } else if (P.x_bytes == 8) {
