@@ -27,6 +27,7 @@
 // sums through distributed shared memory in a fixed order: y is the same on
 // every run. Every wait is bounded by the device timer.
 #include <cooperative_groups.h>
+#include <stddef.h>
 #include <string.h>
 
 #include "wc_q4_core.cuh"
@@ -49,20 +50,28 @@ constexpr uint32_t kSmemMax = 232448;
 
 constexpr int kMWarps = 2;
 constexpr int kWWarp = 0, kMWarp0 = 2;  // 1: activations; 2, 3: MMA issue
-constexpr int kUnpTurns = 2;
-constexpr int kUnpWarp0 = 4;    // 4..11: lane quarter warp % 4, slices in turns
-constexpr int kSclWarp0 = kUnpWarp0 + 4 * kUnpTurns;  // 12..27: lane quarter warp % 4, columns
-constexpr int kSclWarps = 16;
-constexpr int kGemmWarps = kSclWarp0 + kSclWarps;
-constexpr int kQ4GemmThreads = 32 * kGemmWarps;
+constexpr int kUnpWarp0 = 4;    // then the unpacking warps and the scaling warps
 
-// Registers of a thread after the roles split: a scaling warp holds up to 32
-// sums and as many results on their way.
-constexpr int kRegsLaunch = 72, kRegsIssue = 48, kRegsUnpack = 48, kRegsScale = 88;
-static_assert(kQ4GemmThreads * kRegsLaunch <= 65536, "registers at launch");
-static_assert(4 * kRegsIssue + 4 * kUnpTurns * kRegsUnpack + kSclWarps * kRegsScale <=
-                  kGemmWarps * kRegsLaunch,
-              "the roles' registers come out of those at launch");
+// Four unpacking warps a slice, slices in kUnpTurns turns; a scaling warp holds
+// 32 rows' sums of up to 32 columns. Wide tiles spend their time on the sums,
+// narrow ones on the codes: 16 scaling and 8 unpacking warps against 8 and 12 at
+// NT = 128 measured 73 and 84 us (512 rows of x, 4096 x 14336, groups of 64), at
+// NT = 64 20 and 18.5 us (64 rows, 14336 x 4096, groups of 128).
+template <int NT>
+struct Roles {
+    static constexpr int unp_turns = NT == 128 ? 2 : 3;
+    static constexpr int scl_warps = NT == 128 ? 16 : 8;
+    static constexpr int scl_warp0 = kUnpWarp0 + 4 * unp_turns;
+    static constexpr int warps = scl_warp0 + scl_warps;
+    static constexpr int threads = 32 * warps;
+    // Registers of a thread at launch and after the roles split.
+    static constexpr int regs = NT == 128 ? 72 : 80;
+    static constexpr int regs_issue = 48, regs_unpack = 48, regs_scale = NT == 128 ? 88 : 104;
+    static_assert(threads * regs <= 65536, "registers at launch");
+    static_assert(4 * regs_issue + 4 * unp_turns * regs_unpack + scl_warps * regs_scale <=
+                      warps * regs,
+                  "the roles' registers come out of those at launch");
+};
 
 // Accumulators of NT columns: group number n of the block goes to n % accs.
 template <int NT, int PER>
@@ -142,18 +151,37 @@ __device__ __forceinline__ GmUnit unit_at(const GmParams& P, const GmSmem& S, ui
     return t;
 }
 
+// Addresses of the barriers in the shared window, from one base register that the
+// compiler cannot take apart: computed from pointers, each use became a handful of
+// uniform instructions, and the kernel is bound by instruction issue.
+__device__ __forceinline__ uint32_t ctl_base(const GmSmem& S) {
+    uint32_t a;
+    asm volatile("mov.u32 %0, %1;" : "=r"(a) : "r"(smem_addr(S.ctl)));
+    return a;
+}
+#define WC_BAR(field) (cb + uint32_t(offsetof(GmCtl, field)))
+
+__device__ __forceinline__ void bar_arrive(uint32_t bar) {
+    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ void bar_commit(uint32_t bar) {
+    asm volatile(
+        "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar)
+        : "memory");
+}
+
 // One poll, which suspends the thread for a while. Without a time of its own: a
 // poll that names one becomes a loop of polls, sleeps and clock reads (measured
 // here: 350 barrier and 160 sleep instructions a slice instead of some 75), whose
 // instructions the other roles wait for.
-__device__ __forceinline__ bool gm_poll(unsigned long long* bar, uint32_t parity) {
+__device__ __forceinline__ bool gm_poll(uint32_t bar, uint32_t parity) {
     uint32_t done;
     asm volatile(
         "{\n\t.reg .pred p;\n\t"
         "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
         "selp.u32 %0, 1, 0, p;\n\t}"
         : "=r"(done)
-        : "r"(smem_addr(bar)), "r"(parity)
+        : "r"(bar), "r"(parity)
         : "memory");
     return done != 0;
 }
@@ -161,7 +189,7 @@ __device__ __forceinline__ bool gm_poll(unsigned long long* bar, uint32_t parity
 // Wait for a phase; false if another role gave up or the time limit passed. The
 // rare part stays out of the way of the instructions that follow a poll which
 // succeeds at once.
-__device__ __forceinline__ bool gm_wait_more(unsigned long long* bar, uint32_t parity, GmCtl& c,
+__device__ __forceinline__ bool gm_wait_more(uint32_t bar, uint32_t parity, GmCtl& c,
                                              int32_t* status) {
     uint64_t t0 = 0;
     for (;;) {
@@ -183,7 +211,7 @@ __device__ __forceinline__ bool gm_wait_more(unsigned long long* bar, uint32_t p
             "DONE:\n\t"
             "selp.u32 %0, 1, 0, p;\n\t}"
             : "=r"(done)
-            : "r"(smem_addr(bar)), "r"(parity)
+            : "r"(bar), "r"(parity)
             : "memory");
         if (done) return true;
         const uint64_t t = global_timer_ns();
@@ -197,7 +225,7 @@ __device__ __forceinline__ bool gm_wait_more(unsigned long long* bar, uint32_t p
     }
 }
 
-__device__ __forceinline__ bool gm_wait(unsigned long long* bar, uint32_t parity, GmCtl& c,
+__device__ __forceinline__ bool gm_wait(uint32_t bar, uint32_t parity, GmCtl& c,
                                         int32_t* status) {
     if (__builtin_expect(gm_poll(bar, parity), 1)) return true;
     return gm_wait_more(bar, parity, c, status);
@@ -216,7 +244,7 @@ __device__ __forceinline__ bool elect_one() {
 
 // The same by a whole warp: if any lane gives up, all do, so that the warp stays
 // converged for its warp-wide tcgen05 instructions.
-__device__ __forceinline__ bool gm_wait_warp(unsigned long long* bar, uint32_t parity, GmCtl& c,
+__device__ __forceinline__ bool gm_wait_warp(uint32_t bar, uint32_t parity, GmCtl& c,
                                              int32_t* status) {
     if (__builtin_expect(__all_sync(0xFFFFFFFFu, gm_poll(bar, parity)), 1)) return true;
     return __all_sync(0xFFFFFFFFu, gm_wait_more(bar, parity, c, status));
@@ -243,6 +271,7 @@ __device__ __forceinline__ void my_slices(const GmParams& P, uint32_t& s0, uint3
 template <int NT>
 __device__ void gm_load_w(const GmParams& P, const GmSmem& S) {
     GmCtl& c = *S.ctl;
+    const uint32_t cb = ctl_base(S);
     const Q4Layout& L = P.L;
     uint32_t s0, s1, e = 0;
     my_slices(P, s0, s1);
@@ -256,7 +285,7 @@ __device__ void gm_load_w(const GmParams& P, const GmSmem& S) {
         const uint32_t h = min(8u, L.blocks16 - 8 * t.rb);
         if (t.rb == 0 && s0 == 0) q4_check_header(stream, L, P.a.status);
         for (uint32_t s = s0; s < s1; ++s, w.next()) {
-            if (w.round > 0 && !gm_wait(&c.w_empty[w.s], w.empty(), c, P.a.status)) {
+            if (w.round > 0 && !gm_wait(WC_BAR(w_empty) + 8u * (w.s), w.empty(), c, P.a.status)) {
                 ok = false;
                 break;
             }
@@ -276,6 +305,7 @@ __device__ void gm_load_w(const GmParams& P, const GmSmem& S) {
 template <int NT, int PER>
 __device__ void gm_load_x_tma(const GmParams& P, const GmSmem& S) {
     GmCtl& c = *S.ctl;
+    const uint32_t cb = ctl_base(S);
     uint32_t s0, s1, e = 0;
     my_slices(P, s0, s1);
     Ring<kSRing> x;
@@ -285,7 +315,7 @@ __device__ void gm_load_x_tma(const GmParams& P, const GmSmem& S) {
         if (!t.valid) break;
         e = t.e;
         for (uint32_t s = s0; s < s1; ++s, x.next()) {
-            if (x.round > 0 && !gm_wait(&c.s_free[x.s], x.empty(), c, P.a.status)) {
+            if (x.round > 0 && !gm_wait(WC_BAR(s_free) + 8u * (x.s), x.empty(), c, P.a.status)) {
                 ok = false;
                 break;
             }
@@ -315,14 +345,15 @@ __device__ void gm_load_x_tma(const GmParams& P, const GmSmem& S) {
 template <int NT, int PER, int V>
 __device__ void gm_load_x_any(const GmParams& P, const GmSmem& S, uint32_t tid) {
     GmCtl& c = *S.ctl;
+    const uint32_t cb = ctl_base(S);
     uint32_t s0, s1, e = 0;
     my_slices(P, s0, s1);
     Ring<kSRing> x;
     int prev = -1;  // stage not yet handed over
     auto hand_over = [&](int stage) {
         fence_proxy_async_smem();
-        mbar_arrive(&c.g_full[stage][0]);
-        if (PER > 1) mbar_arrive(&c.g_full[stage][PER / 2]);
+        bar_arrive(WC_BAR(g_full) + 32u * (stage) + 8u * (0));
+        if (PER > 1) bar_arrive(WC_BAR(g_full) + 32u * (stage) + 8u * (PER / 2));
     };
     bool ok = true;
     for (uint32_t u = blockIdx.x / P.split; ok; u += gridDim.x / P.split) {
@@ -330,7 +361,7 @@ __device__ void gm_load_x_any(const GmParams& P, const GmSmem& S, uint32_t tid) 
         if (!t.valid) break;
         e = t.e;
         for (uint32_t s = s0; s < s1; ++s, x.next()) {
-            if (x.round > 0 && !gm_wait_warp(&c.s_free[x.s], x.empty(), c, P.a.status)) {
+            if (x.round > 0 && !gm_wait_warp(WC_BAR(s_free) + 8u * (x.s), x.empty(), c, P.a.status)) {
                 ok = false;
                 break;
             }
@@ -393,6 +424,7 @@ __device__ __forceinline__ uint32_t all_slices(const GmParams& P, const GmSmem& 
 template <int NT, bool HALF, int PER>
 __device__ void gm_unpack(const GmParams& P, const GmSmem& S, int wi, int lane) {
     GmCtl& c = *S.ctl;
+    const uint32_t cb = ctl_base(S);
     const Q4Layout& L = P.L;
     const Q4Masks mk = Q4Masks::make<HALF>();
     const uint32_t q = uint32_t(wi) & 3u, turn = uint32_t(wi) >> 2;
@@ -402,9 +434,9 @@ __device__ void gm_unpack(const GmParams& P, const GmSmem& S, int wi, int lane) 
     const uint32_t t_lane = ((32u * q) << 16) + kACol;
     const uint32_t total = all_slices<NT>(P, S);
     const bool zeros = L.zeros != 0;
-    for (uint32_t n = turn; n < total; n += kUnpTurns) {
+    for (uint32_t n = turn; n < total; n += Roles<NT>::unp_turns) {
         const uint32_t ws = n % kWRing, st = n % kSRing;
-        if (!gm_wait_warp(&c.w_full[ws], (n / kWRing) & 1u, c, P.a.status)) return;
+        if (!gm_wait_warp(WC_BAR(w_full) + 8u * (ws), (n / kWRing) & 1u, c, P.a.status)) return;
         uint32_t zp[PER];
 #pragma unroll
         for (int k = 0; k < PER; ++k) {
@@ -416,7 +448,7 @@ __device__ void gm_unpack(const GmParams& P, const GmSmem& S, int wi, int lane) 
             zp[k] = q4_zero_pair<HALF>(z);
         }
         if (n >= kSRing &&
-            !gm_wait_warp(&c.s_free[st], (n / kSRing - 1u) & 1u, c, P.a.status))
+            !gm_wait_warp(WC_BAR(s_free) + 8u * (st), (n / kSRing - 1u) & 1u, c, P.a.status))
             return;
         tc_fence_after();
         // not unrolled: the roles share an instruction cache
@@ -438,8 +470,8 @@ __device__ void gm_unpack(const GmParams& P, const GmSmem& S, int wi, int lane) 
         __syncwarp();
         if (lane == 0) {
 #pragma unroll
-            for (int g = 0; g < PER; ++g) mbar_arrive(&c.g_full[st][g]);
-            mbar_arrive(&c.w_empty[ws]);
+            for (int g = 0; g < PER; ++g) bar_arrive(WC_BAR(g_full) + 32u * (st) + 8u * (g));
+            bar_arrive(WC_BAR(w_empty) + 8u * (ws));
         }
     }
 }
@@ -457,6 +489,7 @@ __device__ void gm_unpack(const GmParams& P, const GmSmem& S, int wi, int lane) 
 template <int NT, bool HALF, int PER, int TURN>
 __device__ void gm_mma(const GmParams& P, const GmSmem& S) {
     GmCtl& c = *S.ctl;
+    const uint32_t cb = ctl_base(S);
     constexpr uint32_t ACCS = accs<NT, PER>();
     constexpr int kGroups = PER == 1 ? 1 : PER / 2;  // of this warp in a slice it takes
     constexpr int kMmas = 8 / PER;                   // a group
@@ -482,7 +515,7 @@ __device__ void gm_mma(const GmParams& P, const GmSmem& S) {
 #pragma unroll
             for (int j = 0; j < kGroups; ++j) {
                 const uint32_t g = PER == 1 ? 0u : TURN * kGroups + j;
-                if (!gm_wait_warp(&c.g_full[st][g], round & 1u, c, P.a.status)) {
+                if (!gm_wait_warp(WC_BAR(g_full) + 32u * (st) + 8u * (g), round & 1u, c, P.a.status)) {
                     ok = false;
                     break;
                 }
@@ -497,8 +530,8 @@ __device__ void gm_mma(const GmParams& P, const GmSmem& S) {
                         umma_bf16_ts(acc, a0 + 8u * k,
                                      PER == 1 && k >= 4 ? xd1 + 2u * (k - 4) : b0 + 2u * k, idesc,
                                      k > 0 ? 1u : 0u);
-                    umma_commit(&c.done[st][g]);
-                    if (j == kGroups - 1) umma_commit(&c.s_free[st]);
+                    bar_commit(WC_BAR(done) + 32u * (st) + 8u * (g));
+                    if (j == kGroups - 1) bar_commit(WC_BAR(s_free) + 8u * (st));
                 }
                 __syncwarp();
                 issued = true;
@@ -508,7 +541,7 @@ __device__ void gm_mma(const GmParams& P, const GmSmem& S) {
     }
     if (issued) {  // every MMA has finished before the block ends (elect.sync picks one lane
                    // throughout, so the commit covers all of the warp's)
-        if (elect_one()) umma_commit(&c.drain[TURN]);
+        if (elect_one()) bar_commit(WC_BAR(drain) + 8u * (TURN));
         mbar_wait(&c.drain[TURN], 0, nullptr);
     }
 }
@@ -590,27 +623,6 @@ __device__ __forceinline__ void scale_add(uint64_t (&sum)[8], uint32_t taddr, ui
         : "memory");
 }
 
-__device__ __forceinline__ void scale_add(uint64_t (&sum)[4], uint32_t taddr, uint32_t bar,
-                                          uint32_t arrive, uint64_t s2) {
-    asm volatile(
-        "{\n\t.reg .b32 v<8>;\n\t.reg .b64 p;\n\t.reg .pred f;\n\t"
-        "tcgen05.ld.sync.aligned.32x32b.x8.b32 {"
-        "v0,v1,v2,v3,v4,v5,v6,v7}, [%4];\n\t"
-        "tcgen05.wait::ld.sync.aligned;\n\t"
-        "tcgen05.fence::before_thread_sync;\n\t"
-        "bar.warp.sync 0xFFFFFFFF;\n\t"
-        "setp.ne.u32 f, %6, 0;\n\t"
-        "@f mbarrier.arrive.shared::cta.b64 _, [%5];\n\t"
-        "mov.b64 p, {v0, v1};\n\tfma.rn.f32x2 %0, %7, p, %0;\n\t"
-        "mov.b64 p, {v2, v3};\n\tfma.rn.f32x2 %1, %7, p, %1;\n\t"
-        "mov.b64 p, {v4, v5};\n\tfma.rn.f32x2 %2, %7, p, %2;\n\t"
-        "mov.b64 p, {v6, v7};\n\tfma.rn.f32x2 %3, %7, p, %3;\n\t"
-        "}"
-        : "+l"(sum[0]), "+l"(sum[1]), "+l"(sum[2]), "+l"(sum[3])
-        : "r"(taddr), "r"(bar), "r"(arrive), "l"(s2)
-        : "memory");
-}
-
 __device__ __forceinline__ uint64_t pair2(float s) {
     uint64_t d;
     asm("mov.b64 %0, {%1, %1};" : "=l"(d) : "f"(s));
@@ -623,9 +635,10 @@ __device__ __forceinline__ float half2f(uint64_t v, int hi) {
 template <int NT, bool HALF, int PER>
 __device__ void gm_scale(const GmParams& P, const GmSmem& S, int wi, int lane) {
     GmCtl& c = *S.ctl;
+    const uint32_t cb = ctl_base(S);
     const Q4Layout& L = P.L;
     constexpr uint32_t ACCS = accs<NT, PER>();
-    constexpr int HN = NT / (kSclWarps / 4);  // columns of this warp
+    constexpr int HN = NT / (Roles<NT>::scl_warps / 4);  // columns of this warp
     const uint32_t q = uint32_t(wi) & 3u, part = uint32_t(wi) >> 2;
     const uint32_t r = 32u * q + uint32_t(lane);
     const uint32_t scale_at = smem_addr(S.w) + (r >> 4) * L.rec + kQ4Codes + (r & 15u) * 2u;
@@ -634,7 +647,7 @@ __device__ void gm_scale(const GmParams& P, const GmSmem& S, int wi, int lane) {
     uint32_t s0, s1, e = 0, count = 0;
     my_slices(P, s0, s1);
     if (lane == 0)  // the first groups' accumulators are free
-        for (uint32_t k = 0; k < ACCS; ++k) mbar_arrive(&c.g_full[k / PER][k % PER]);
+        for (uint32_t k = 0; k < ACCS; ++k) bar_arrive(WC_BAR(g_full) + 32u * (k / PER) + 8u * (k % PER));
     for (uint32_t u = blockIdx.x / P.split;; u += gridDim.x / P.split) {
         const GmUnit t = unit_at<NT>(P, S, u, e);
         if (!t.valid) return;
@@ -648,7 +661,7 @@ __device__ void gm_scale(const GmParams& P, const GmSmem& S, int wi, int lane) {
 #pragma unroll
             for (int g = 0; g < PER; ++g) {
                 const uint32_t gi = count * PER + g, next = gi + ACCS;
-                if (!gm_wait_warp(&c.done[st][g], round & 1u, c, P.a.status)) return;
+                if (!gm_wait_warp(WC_BAR(done) + 32u * (st) + 8u * (g), round & 1u, c, P.a.status)) return;
                 tc_fence_after();
                 // The group's MMAs are done, so its records have long landed
                 // (the unpacking warps waited for them) and stay until this
@@ -658,15 +671,16 @@ __device__ void gm_scale(const GmParams& P, const GmSmem& S, int wi, int lane) {
                              : "=h"(bits)
                              : "r"(scale_at + ws * kWStage + 32u * g));
                 const uint64_t sc = pair2(q4_scale(bits, half_scales));
-                unsigned long long* bar = &c.g_full[next / PER % kSRing][next % PER];
+                const uint32_t bar =
+                    WC_BAR(g_full) + 32u * (next / PER % kSRing) + 8u * (next % PER);
                 if (live > 0) {
-                    scale_add(sum, t_lane + gi % ACCS * NT, smem_addr(bar), lane == 0, sc);
+                    scale_add(sum, t_lane + gi % ACCS * NT, bar, lane == 0, sc);
                 } else {
-                    if (lane == 0) mbar_arrive(bar);
+                    if (lane == 0) bar_arrive(bar);
                 }
                 if (g == PER - 1) {
                     __syncwarp();
-                    if (lane == 0) mbar_arrive(&c.w_empty[ws]);
+                    if (lane == 0) bar_arrive(WC_BAR(w_empty) + 8u * (ws));
                 }
             }
         }
@@ -689,7 +703,7 @@ __device__ void gm_scale(const GmParams& P, const GmSmem& S, int wi, int lane) {
 }
 
 template <int NT, bool HALF, int PER>
-__global__ void __launch_bounds__(kQ4GemmThreads, 1)
+__global__ void __launch_bounds__(Roles<NT>::threads, 1)
     q4_gemm_kernel(const __grid_constant__ GmParams P) {
     extern __shared__ __align__(1024) unsigned char smem_raw[];
     const int tid = threadIdx.x, lane = tid & 31;
@@ -709,13 +723,13 @@ __global__ void __launch_bounds__(kQ4GemmThreads, 1)
     if (tid == 0) {
         for (uint32_t s = 0; s < kWRing; ++s) {
             mbar_init(&c.w_full[s], 1);
-            mbar_init(&c.w_empty[s], 4 + kSclWarps);
+            mbar_init(&c.w_empty[s], 4 + Roles<NT>::scl_warps);
         }
         for (uint32_t s = 0; s < kSRing; ++s) {
             for (int g = 0; g < PER; ++g) {
                 const bool first = g == 0 || (PER > 1 && g == PER / 2);  // of a panel
                 mbar_init(&c.g_full[s][g],
-                          4 + kSclWarps + (!first ? 0 : P.x_bytes == 16 ? 1 : 32));
+                          4 + Roles<NT>::scl_warps + (!first ? 0 : P.x_bytes == 16 ? 1 : 32));
                 mbar_init(&c.done[s][g], 1);
             }
             mbar_init(&c.s_free[s], PER == 1 ? 1 : kMWarps);
@@ -733,7 +747,7 @@ __global__ void __launch_bounds__(kQ4GemmThreads, 1)
     }
     if (P.a.offsets != nullptr) {  // the experts' rows and first units
         const int total = int(P.a.tokens);
-        for (uint32_t e = tid; e < P.a.experts; e += kQ4GemmThreads) {
+        for (uint32_t e = tid; e < P.a.experts; e += Roles<NT>::threads) {
             const int lo = min(max(P.a.offsets[e], 0), total);
             const int hi = min(max(P.a.offsets[e + 1], lo), total);
             const uint32_t cnt = uint32_t(hi - lo);
@@ -770,7 +784,7 @@ __global__ void __launch_bounds__(kQ4GemmThreads, 1)
     }
 
     if (warp < kUnpWarp0) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsIssue));
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(Roles<NT>::regs_issue));
         if (warp == kWWarp) {
             if (lane == 0) gm_load_w<NT>(P, S);
         } else if (warp >= kMWarp0) {
@@ -788,17 +802,17 @@ __global__ void __launch_bounds__(kQ4GemmThreads, 1)
             gm_load_x_any<NT, PER, 2>(P, S, lane);
         }
         __syncthreads();  // (no warp spins for the registers that the scaling warps hold)
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsLaunch));
-    } else if (warp < kSclWarp0) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsUnpack));
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(Roles<NT>::regs));
+    } else if (warp < Roles<NT>::scl_warp0) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(Roles<NT>::regs_unpack));
         gm_unpack<NT, HALF, PER>(P, S, warp - kUnpWarp0, lane);
         __syncthreads();
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsLaunch));
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(Roles<NT>::regs));
     } else {
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsScale));
-        gm_scale<NT, HALF, PER>(P, S, warp - kSclWarp0, lane);
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(Roles<NT>::regs_scale));
+        gm_scale<NT, HALF, PER>(P, S, warp - Roles<NT>::scl_warp0, lane);
         __syncthreads();
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsLaunch));
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(Roles<NT>::regs));
     }
     __syncwarp();
     if (P.split > 1) {
@@ -810,7 +824,7 @@ __global__ void __launch_bounds__(kQ4GemmThreads, 1)
             const uint32_t rank = blockIdx.x % P.split;
             const float* red = reinterpret_cast<const float*>(S.x);
             const uint32_t t0 = t.ntok * rank / P.split, t1 = t.ntok * (rank + 1) / P.split;
-            for (uint32_t k = t0 * kRowsTile + tid; k < t1 * kRowsTile; k += kQ4GemmThreads) {
+            for (uint32_t k = t0 * kRowsTile + tid; k < t1 * kRowsTile; k += Roles<NT>::threads) {
                 float v = 0.f;
                 for (uint32_t b = 0; b < P.split; ++b) v += cluster.map_shared_rank(red, b)[k];
                 const uint32_t row = t.rb * kRowsTile + k % kRowsTile;
@@ -855,7 +869,7 @@ cudaError_t gm_launch(GmParams& P, uint32_t sms, uint32_t units, cudaStream_t st
     }
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(P.split > 1 ? units * P.split : units < sms ? units : sms);
-    cfg.blockDim = dim3(kQ4GemmThreads);
+    cfg.blockDim = dim3(Roles<NT>::threads);
     cfg.dynamicSmemBytes = gm_smem<NT>(P.a.experts);
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
