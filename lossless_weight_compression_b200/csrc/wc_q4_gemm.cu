@@ -66,7 +66,8 @@ struct Roles {
     static constexpr int threads = 32 * warps;
     // Registers of a thread at launch and after the roles split.
     static constexpr int regs = NT == 128 ? 72 : 80;
-    static constexpr int regs_issue = 48, regs_unpack = 48, regs_scale = NT == 128 ? 88 : 104;
+    static constexpr int regs_issue = NT == 128 ? 56 : 64, regs_unpack = regs_issue;
+    static constexpr int regs_scale = NT == 128 ? 80 : 104;
     static_assert(threads * regs <= 65536, "registers at launch");
     static_assert(4 * regs_issue + 4 * unp_turns * regs_unpack + scl_warps * regs_scale <=
                       warps * regs,
@@ -186,34 +187,14 @@ __device__ __forceinline__ bool gm_poll(uint32_t bar, uint32_t parity) {
     return done != 0;
 }
 
-// Wait for a phase; false if another role gave up or the time limit passed. The
-// rare part stays out of the way of the instructions that follow a poll which
-// succeeds at once.
-__device__ __forceinline__ bool gm_wait_more(uint32_t bar, uint32_t parity, GmCtl& c,
-                                             int32_t* status) {
+// Wait for a phase (one lane); false if another role gave up or the time limit
+// passed.
+__device__ __forceinline__ bool gm_wait(uint32_t bar, uint32_t parity, GmCtl& c, int32_t* status) {
     uint64_t t0 = 0;
     for (;;) {
-        // polls are the only instructions of this loop: what a waiting warp
-        // issues, the others of its scheduler do not
-        uint32_t done;
-        asm volatile(
-            "{\n\t.reg .pred p;\n\t.reg .u32 k;\n\t"
-            "mov.u32 k, 64;\n\t"
-            "MORE:\n\t"
-            "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t@p bra DONE;\n\t"
-            "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t@p bra DONE;\n\t"
-            "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t@p bra DONE;\n\t"
-            "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t@p bra DONE;\n\t"
-            "sub.u32 k, k, 1;\n\t"
-            "setp.ne.u32 p, k, 0;\n\t"
-            "@p bra MORE;\n\t"
-            "setp.ne.u32 p, k, k;\n\t"
-            "DONE:\n\t"
-            "selp.u32 %0, 1, 0, p;\n\t}"
-            : "=r"(done)
-            : "r"(bar), "r"(parity)
-            : "memory");
-        if (done) return true;
+#pragma unroll 1
+        for (int k = 0; k < 128; ++k)
+            if (gm_poll(bar, parity)) return true;
         const uint64_t t = global_timer_ns();
         if (t0 == 0) t0 = t;
         if (*const_cast<volatile int*>(&c.abort)) return false;
@@ -223,12 +204,6 @@ __device__ __forceinline__ bool gm_wait_more(uint32_t bar, uint32_t parity, GmCt
             return false;
         }
     }
-}
-
-__device__ __forceinline__ bool gm_wait(uint32_t bar, uint32_t parity, GmCtl& c,
-                                        int32_t* status) {
-    if (__builtin_expect(gm_poll(bar, parity), 1)) return true;
-    return gm_wait_more(bar, parity, c, status);
 }
 
 // True in one lane of the (converged) warp.
@@ -242,12 +217,26 @@ __device__ __forceinline__ bool elect_one() {
     return e != 0;
 }
 
-// The same by a whole warp: if any lane gives up, all do, so that the warp stays
-// converged for its warp-wide tcgen05 instructions.
+// The same by a whole warp, its control flow uniform throughout: the lanes' polls
+// may differ, but no lane goes on before a vote, so that the warp reaches the
+// warp-wide (.aligned) instructions that follow as one.
 __device__ __forceinline__ bool gm_wait_warp(uint32_t bar, uint32_t parity, GmCtl& c,
                                              int32_t* status) {
     if (__builtin_expect(__all_sync(0xFFFFFFFFu, gm_poll(bar, parity)), 1)) return true;
-    return __all_sync(0xFFFFFFFFu, gm_wait_more(bar, parity, c, status));
+    uint64_t t0 = 0;
+    for (;;) {
+#pragma unroll 1
+        for (int k = 0; k < 128; ++k)
+            if (__all_sync(0xFFFFFFFFu, gm_poll(bar, parity))) return true;
+        const uint64_t t = global_timer_ns();
+        if (t0 == 0) t0 = t;
+        const bool late = t - t0 > kWaitLimitNs;
+        if (__any_sync(0xFFFFFFFFu, late || *const_cast<volatile int*>(&c.abort))) {
+            if (late) report(status, kStatusTimeout);
+            c.abort = 1;
+            return false;
+        }
+    }
 }
 
 // A ring position: stage and how often the ring went round.
@@ -542,7 +531,10 @@ __device__ void gm_mma(const GmParams& P, const GmSmem& S) {
     if (issued) {  // every MMA has finished before the block ends (elect.sync picks one lane
                    // throughout, so the commit covers all of the warp's)
         if (elect_one()) bar_commit(WC_BAR(drain) + 8u * (TURN));
-        mbar_wait(&c.drain[TURN], 0, nullptr);
+        __syncwarp();
+        // (also after a role gave up: what was issued has to end, and does)
+        for (int k = 0; k < (1 << 20); ++k)
+            if (__all_sync(0xFFFFFFFFu, gm_poll(WC_BAR(drain) + 8u * (TURN), 0))) break;
     }
 }
 
@@ -801,6 +793,7 @@ __global__ void __launch_bounds__(Roles<NT>::threads, 1)
         } else {
             gm_load_x_any<NT, PER, 2>(P, S, lane);
         }
+        __syncwarp();     // (of roles that one lane takes)
         __syncthreads();  // (no warp spins for the registers that the scaling warps hold)
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(Roles<NT>::regs));
     } else if (warp < Roles<NT>::scl_warp0) {
