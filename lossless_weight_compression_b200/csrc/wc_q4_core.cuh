@@ -165,6 +165,16 @@ struct Q4GemmArgs {
     int32_t* status;
 };
 
+// Result y[row of x][row of W], rounded once if it is to be 16 bits.
+template <bool HALF>
+__device__ __forceinline__ void q4_store(const Q4GemmArgs& a, uint64_t tok, uint32_t row, float v) {
+    if (a.flags & kQ4Y16)
+        static_cast<uint16_t*>(a.y)[tok * a.ldy + row] =
+            HALF ? __half_as_ushort(__float2half_rn(v)) : __bfloat16_as_ushort(__float2bfloat16_rn(v));
+    else
+        static_cast<float*>(a.y)[tok * a.ldy + row] = v;
+}
+
 cudaError_t launch_q4_quantize(const void* w, uint64_t ld, const Q4Layout& L, uint8_t* out,
                                cudaStream_t stream);
 cudaError_t launch_q4_pack(const uint8_t* codes, const void* scales, const uint8_t* zeros,

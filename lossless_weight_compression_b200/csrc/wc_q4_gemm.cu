@@ -538,15 +538,6 @@ __device__ void gm_mma(const GmParams& P, const GmSmem& S) {
     }
 }
 
-template <bool HALF>
-__device__ __forceinline__ void store_y(const GmParams& P, uint64_t tok, uint32_t row, float v) {
-    if (P.a.flags & kQ4Y16)
-        static_cast<uint16_t*>(P.a.y)[tok * P.a.ldy + row] =
-            HALF ? __half_as_ushort(__float2half_rn(v)) : __bfloat16_as_ushort(__float2bfloat16_rn(v));
-    else
-        static_cast<float*>(P.a.y)[tok * P.a.ldy + row] = v;
-}
-
 // A group's results (consecutive FP32 columns of this thread's tensor memory
 // lane) scaled and added to the sums, two a instruction, each FMA rounded to
 // nearest; once they are read, one lane says so on `bar`. One block of assembly,
@@ -682,7 +673,7 @@ __device__ void gm_scale(const GmParams& P, const GmSmem& S, int wi, int lane) {
 #pragma unroll
                 for (int k = 0; k < HN; ++k)
                     if (uint32_t(k) < live)
-                        store_y<HALF>(P, uint64_t(t.tok0) + part * HN + k, row,
+                        q4_store<HALF>(P.a, uint64_t(t.tok0) + part * HN + k, row,
                                       half2f(sum[k / 2], k & 1));
             }
         } else {  // the block's only unit: every copy into the ring has been used
@@ -821,7 +812,7 @@ __global__ void __launch_bounds__(Roles<NT>::threads, 1)
                 float v = 0.f;
                 for (uint32_t b = 0; b < P.split; ++b) v += cluster.map_shared_rank(red, b)[k];
                 const uint32_t row = t.rb * kRowsTile + k % kRowsTile;
-                if (row < P.L.rows) store_y<HALF>(P, uint64_t(t.tok0) + k / kRowsTile, row, v);
+                if (row < P.L.rows) q4_store<HALF>(P.a, uint64_t(t.tok0) + k / kRowsTile, row, v);
             }
         }
         cluster.sync();

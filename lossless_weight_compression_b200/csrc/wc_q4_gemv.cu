@@ -8,8 +8,24 @@
 // 16-row operand and up to 8 rows of x as the 8 columns; each group's sum is
 // then scaled once into a second FP32 accumulator. So no scaled weight is ever
 // rounded, and a weight costs about 1.4 instructions. At these row counts the
-// time is the stream's bytes.
+// time is the stream's bytes and how soon they are on their way: a thread block
+// owns 128 weight rows (the blocks of a cluster share their slices of 128
+// columns), and a producer warp keeps up to eight slices' records in flight,
+// each one contiguous bulk copy, beside the slice's activations. Eight warps
+// take one 16-row record each, so that the only sum across warps is the
+// cluster's, over its blocks in a fixed order.
+//
+// Measured (GPU time, groups of 128, BF16; beside it the time of the bytes at the
+// copy's rate): 1 row of x through 4096 x 4096 6.3 us (1.3), through 4096 x 14336
+// 13.5 us (4.7); 8 rows through 14336 x 4096 15.9 us (4.7), 16 rows 20 us; 48 rows
+// over 43 of 64 experts of 2048 x 1024 17 us (8.3). Bound by the warps' chains of
+// unpacking and multiplying (issue 53 %), and the smallest by a launch's latency.
+// Loads straight into registers, with a row's slices spread over a block's warps,
+// were 10 % faster for one row of x through 4096 x 4096, 10 to 60 % slower for
+// experts and for 16 rows. Two sums a group instead of one, for shorter chains of
+// matrix instructions: no gain, 15 % slower at 16 rows (registers).
 #include <cooperative_groups.h>
+#include <stddef.h>
 
 #include <mutex>
 
@@ -20,16 +36,107 @@ namespace {
 
 namespace cg = cooperative_groups;
 
-constexpr int kWarps = 8;
-constexpr int kGvThreads = 32 * kWarps;
+constexpr int kGvWarps = 8;                         // one record each
+constexpr int kGvThreads = 32 * (kGvWarps + 1);     // and the producer
+constexpr uint32_t kGvMaxStages = 8;
 
 struct GvParams {
     Q4GemmArgs a;
     Q4Layout L;
-    uint32_t wk;       // warps that share a row group's slices (a power of two up to 8)
-    uint32_t split;    // thread blocks of a cluster that share them, too
+    uint32_t split;    // thread blocks of a cluster, which share the slices
     uint32_t x_bytes;  // bytes (2 to 16) that divide the address of every row of x
+    uint32_t pitch;    // bytes of a stage's records
 };
+
+struct GvCtl {
+    unsigned long long full[kGvMaxStages], empty[kGvMaxStages];
+    int abort;
+};
+
+// NT x 8 rows of x; a stage's activations are 256 bytes a row.
+template <int NT>
+struct GvShape {
+    static constexpr uint32_t stages = NT == 1 ? 8 : 7;  // two blocks fit a multiprocessor
+    static constexpr uint32_t x_bytes = NT * 8 * 256;
+    static constexpr uint32_t vals = NT * 4 * 32;        // results of a record
+};
+
+template <int NT>
+__host__ __device__ inline uint32_t gv_smem(uint32_t pitch) {
+    return GvShape<NT>::stages * (pitch + GvShape<NT>::x_bytes) + kGvWarps * GvShape<NT>::vals * 4 +
+           uint32_t((sizeof(GvCtl) + 15) / 16 * 16);
+}
+
+__device__ __forceinline__ bool gv_poll(unsigned long long* bar, uint32_t parity) {
+    uint32_t done;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(done)
+        : "r"(smem_addr(bar)), "r"(parity)
+        : "memory");
+    return done != 0;
+}
+
+// Wait of a whole warp for a phase, its control flow uniform; false if another
+// warp gave up or the time limit passed.
+__device__ __forceinline__ bool gv_wait(unsigned long long* bar, uint32_t parity, GvCtl& c,
+                                        int32_t* status) {
+    uint64_t t0 = 0;
+    for (;;) {
+#pragma unroll 1
+        for (int k = 0; k < 128; ++k)
+            if (__all_sync(0xFFFFFFFFu, gv_poll(bar, parity))) return true;
+        const uint64_t t = global_timer_ns();
+        if (t0 == 0) t0 = t;
+        const bool late = t - t0 > kWaitLimitNs;
+        if (__any_sync(0xFFFFFFFFu, late || *const_cast<volatile int*>(&c.abort))) {
+            if (late) report(status, kStatusTimeout);
+            c.abort = 1;
+            return false;
+        }
+    }
+}
+
+// Byte b of row n of a stage's activations: 16-byte pieces, those of odd rows
+// swapped in fours, so that the eight lanes of two rows read all banks.
+__device__ __forceinline__ uint32_t gv_x_at(uint32_t n, uint32_t b) {
+    return n * 256u + (b ^ ((n & 1u) << 6));
+}
+
+// The slice's activations by V-byte copies (16, 8, 4: cp.async; 2: through
+// registers), zeros past the last column. Rows past the range are not copied:
+// whatever their columns of the product hold is not stored.
+template <int V>
+__device__ __forceinline__ void gv_copy_x(const GvParams& P, uint32_t dst, uint32_t t0, uint32_t ntok,
+                                          uint32_t s, uint32_t lane) {
+    constexpr uint32_t W = V == 2 ? 4 : V;
+    constexpr uint32_t per_row = 256 / W;
+    for (uint32_t k = lane; k < ntok * per_row; k += 32) {
+        const uint32_t n = k / per_row, b = (k % per_row) * W;
+        const uint32_t col = s * kQ4Cols + b / 2;
+        const uint16_t* src =
+            static_cast<const uint16_t*>(P.a.x) + uint64_t(t0 + n) * P.a.ldx + col;
+        const uint32_t have = col < P.L.cols ? min(W, (P.L.cols - col) * 2) : 0u;
+        const uint32_t at = dst + gv_x_at(n, b);
+        if (V == 2) {
+            const uint32_t v = (have >= 2 ? uint32_t(src[0]) : 0u) |
+                               (have >= 4 ? uint32_t(src[1]) << 16 : 0u);
+            asm volatile("st.shared.u32 [%0], %1;" ::"r"(at), "r"(v) : "memory");
+        } else {
+            const void* from = have ? static_cast<const void*>(src) : P.a.x;
+            if (V == 16)
+                asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(at), "l"(from),
+                             "r"(have)
+                             : "memory");
+            else
+                asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(at), "l"(from),
+                             "n"(V == 2 ? 4 : V == 16 ? 4 : V), "r"(have)
+                             : "memory");
+        }
+    }
+}
 
 template <bool HALF>
 __device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
@@ -46,133 +153,87 @@ __device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1
             : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// Eight activations of a row from column c, zeros past the end.
-__device__ __forceinline__ uint4 load_x8(const uint16_t* row, uint32_t c, uint32_t cols,
-                                         uint32_t x_bytes) {
-    if (x_bytes >= 4 && c + 8 <= cols) {
-        if (x_bytes == 16) return __ldg(reinterpret_cast<const uint4*>(row + c));
-        if (x_bytes == 8) {
-            const uint2 a = __ldg(reinterpret_cast<const uint2*>(row + c));
-            const uint2 b = __ldg(reinterpret_cast<const uint2*>(row + c + 4));
-            return make_uint4(a.x, a.y, b.x, b.y);
-        }
-        const uint32_t* p = reinterpret_cast<const uint32_t*>(row + c);
-        return make_uint4(__ldg(p), __ldg(p + 1), __ldg(p + 2), __ldg(p + 3));
-    }
-    uint32_t v[4] = {0, 0, 0, 0};
-#pragma unroll
-    for (uint32_t k = 0; k < 8; ++k)
-        if (c + k < cols) v[k >> 1] |= uint32_t(__ldg(row + c + k)) << (16 * (k & 1));
-    return make_uint4(v[0], v[1], v[2], v[3]);
-}
-
 __device__ __forceinline__ uint32_t word_of(const uint4& v, int i) {
     return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w;
 }
 
-// What a warp reads of one slice: RT 16-row records (each lane 16 bytes of codes
-// of the rows g and g + 8, their scales and zero points) and NT x 8 rows of x.
-template <int RT, int NT, int PER>
-struct Slice {
-    uint4 c0[RT], c1[RT], x[NT][4];
-    uint16_t s0[RT][PER], s1[RT][PER];
-    uint8_t z0[RT][PER], z1[RT][PER];
-};
-
-template <int RT, int NT, int PER>
-__device__ __forceinline__ void load_slice(Slice<RT, NT, PER>& v, const GvParams& P,
-                                           const uint8_t* stream, uint32_t b0, uint32_t s,
-                                           uint32_t nrec, uint32_t t0, uint32_t hi, uint32_t g,
-                                           uint32_t t) {
-    const Q4Layout& L = P.L;
-    const uint8_t* rec = stream + q4_record(L, b0, s);
-#pragma unroll
-    for (int r = 0; r < RT; ++r) {
-        const uint8_t* p = rec + (uint32_t(r) < nrec ? r : 0) * L.rec;
-        v.c0[r] = ld_stream_v4(p + t * 256 + g * 16);
-        v.c1[r] = ld_stream_v4(p + t * 256 + g * 16 + 128);
-        const uint16_t* sp = reinterpret_cast<const uint16_t*>(p + kQ4Codes);
-#pragma unroll
-        for (int k = 0; k < PER; ++k) {
-            v.s0[r][k] = __ldg(sp + k * 16 + g);
-            v.s1[r][k] = __ldg(sp + k * 16 + g + 8);
-            const uint8_t* zp = p + kQ4Codes + 32 * PER + k * 16 + g;
-            v.z0[r][k] = L.zeros ? __ldg(zp) : 8u;
-            v.z1[r][k] = L.zeros ? __ldg(zp + 8) : 8u;
-        }
-    }
-#pragma unroll
-    for (int n = 0; n < NT; ++n) {
-        const uint32_t tok = t0 + 8 * n + g;
-        const uint16_t* row = static_cast<const uint16_t*>(P.a.x) + uint64_t(tok) * P.a.ldx;
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-            v.x[n][i] = tok < hi ? load_x8(row, s * kQ4Cols + 32 * i + 8 * t, L.cols, P.x_bytes)
-                                 : make_uint4(0, 0, 0, 0);
-    }
+__device__ __forceinline__ uint4 gv_lds128(uint32_t a) {
+    uint4 v;
+    asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "r"(a));
+    return v;
 }
 
-template <bool HALF, int RT, int NT, int PER>
-__device__ __forceinline__ void slice_mma(const Slice<RT, NT, PER>& v, uint32_t half_scales,
-                                          const Q4Masks& mk, float (&acc)[RT][NT][4]) {
+// One record of a slice (at `rec` in shared memory) against NT x 8 rows of x.
+template <bool HALF, int NT, int PER>
+__device__ __forceinline__ void record_mma(uint32_t rec, uint32_t x, uint32_t zeros,
+                                           uint32_t half_scales, uint32_t g, uint32_t t,
+                                           const Q4Masks& mk, float (&acc)[NT][4]) {
+    const uint4 c0 = gv_lds128(rec + t * 256 + g * 16);
+    const uint4 c1 = gv_lds128(rec + t * 256 + g * 16 + 128);
 #pragma unroll
-    for (int g = 0; g < PER; ++g) {
-        float part[RT][NT][4];
+    for (int k = 0; k < PER; ++k) {
+        uint16_t b0, b1;
+        const uint32_t sp = rec + kQ4Codes + (k * 16 + g) * 2;
+        asm volatile("ld.shared.u16 %0, [%1];" : "=h"(b0) : "r"(sp));
+        asm volatile("ld.shared.u16 %0, [%1];" : "=h"(b1) : "r"(sp + 16));
+        uint32_t z0 = 8, z1 = 8;
+        if (zeros) {
+            const uint32_t zp = rec + kQ4Codes + 32 * PER + k * 16 + g;
+            asm volatile("ld.shared.u8 %0, [%1];" : "=r"(z0) : "r"(zp));
+            asm volatile("ld.shared.u8 %0, [%1];" : "=r"(z1) : "r"(zp + 8));
+        }
+        const uint32_t p0 = q4_zero_pair<HALF>(z0), p1 = q4_zero_pair<HALF>(z1);
+        float part[NT][4];
 #pragma unroll
-        for (int r = 0; r < RT; ++r)
+        for (int n = 0; n < NT; ++n)
 #pragma unroll
-            for (int n = 0; n < NT; ++n)
+            for (int j = 0; j < 4; ++j) part[n][j] = 0.f;
 #pragma unroll
-                for (int k = 0; k < 4; ++k) part[r][n][k] = 0.f;
+        for (int i = k * (4 / PER); i < (k + 1) * (4 / PER); ++i) {
+            const uint32_t w0 = word_of(c0, i), w1 = word_of(c1, i);
+            uint4 xv[NT];
 #pragma unroll
-        for (int i = g * (4 / PER); i < (g + 1) * (4 / PER); ++i) {
+            for (int n = 0; n < NT; ++n) xv[n] = gv_lds128(x + gv_x_at(8 * n + g, 64 * i + 16 * t));
 #pragma unroll
-            for (int r = 0; r < RT; ++r) {
-                const uint32_t w0 = word_of(v.c0[r], i), w1 = word_of(v.c1[r], i);
-                const uint32_t z0 = q4_zero_pair<HALF>(v.z0[r][g]);
-                const uint32_t z1 = q4_zero_pair<HALF>(v.z1[r][g]);
+            for (int m = 0; m < 2; ++m) {
+                const uint32_t a0 = q4_pair<HALF>(w0, 2 * m, p0, mk);
+                const uint32_t a1 = q4_pair<HALF>(w1, 2 * m, p1, mk);
+                const uint32_t a2 = q4_pair<HALF>(w0, 2 * m + 1, p0, mk);
+                const uint32_t a3 = q4_pair<HALF>(w1, 2 * m + 1, p1, mk);
 #pragma unroll
-                for (int m = 0; m < 2; ++m) {
-                    const uint32_t a0 = q4_pair<HALF>(w0, 2 * m, z0, mk);
-                    const uint32_t a1 = q4_pair<HALF>(w1, 2 * m, z1, mk);
-                    const uint32_t a2 = q4_pair<HALF>(w0, 2 * m + 1, z0, mk);
-                    const uint32_t a3 = q4_pair<HALF>(w1, 2 * m + 1, z1, mk);
-#pragma unroll
-                    for (int n = 0; n < NT; ++n)
-                        mma16816<HALF>(part[r][n], a0, a1, a2, a3, word_of(v.x[n][i], 2 * m),
-                                       word_of(v.x[n][i], 2 * m + 1));
-                }
+                for (int n = 0; n < NT; ++n)
+                    mma16816<HALF>(part[n], a0, a1, a2, a3, word_of(xv[n], 2 * m),
+                                   word_of(xv[n], 2 * m + 1));
             }
         }
+        const float f0 = q4_scale(b0, half_scales), f1 = q4_scale(b1, half_scales);
 #pragma unroll
-        for (int r = 0; r < RT; ++r) {
-            const float f0 = q4_scale(v.s0[r][g], half_scales), f1 = q4_scale(v.s1[r][g], half_scales);
-#pragma unroll
-            for (int n = 0; n < NT; ++n) {
-                acc[r][n][0] = fmaf(f0, part[r][n][0], acc[r][n][0]);
-                acc[r][n][1] = fmaf(f0, part[r][n][1], acc[r][n][1]);
-                acc[r][n][2] = fmaf(f1, part[r][n][2], acc[r][n][2]);
-                acc[r][n][3] = fmaf(f1, part[r][n][3], acc[r][n][3]);
-            }
+        for (int n = 0; n < NT; ++n) {
+            acc[n][0] = fmaf(f0, part[n][0], acc[n][0]);
+            acc[n][1] = fmaf(f0, part[n][1], acc[n][1]);
+            acc[n][2] = fmaf(f1, part[n][2], acc[n][2]);
+            acc[n][3] = fmaf(f1, part[n][3], acc[n][3]);
         }
     }
 }
 
-// A block's 8 warps are 8 / wk row groups of RT records each, times wk warps
-// that take the row group's slices in turns (the blocks of a cluster, too). The
-// next slice is on its way while one is multiplied.
-template <bool HALF, int RT, int NT, int PER>
+template <bool HALF, int NT, int PER>
 __global__ void __launch_bounds__(kGvThreads, 2) q4_gemv_kernel(const __grid_constant__ GvParams P) {
+    extern __shared__ __align__(128) unsigned char smem_raw[];
     const Q4Layout& L = P.L;
     const Q4GemmArgs& A = P.a;
-    constexpr int kVals = RT * NT * 4 * 32;  // results of a row group, padding included
-    __shared__ float sums[kWarps][kVals];
-    const uint32_t lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    using Shape = GvShape<NT>;
+    uint8_t* w_ring = smem_raw;
+    uint8_t* x_ring = w_ring + Shape::stages * P.pitch;
+    float* sums = reinterpret_cast<float*>(x_ring + Shape::stages * Shape::x_bytes);
+    GvCtl& c = *reinterpret_cast<GvCtl*>(sums + kGvWarps * Shape::vals);
+    const uint32_t lane = threadIdx.x & 31;
+    const uint32_t warp = __shfl_sync(0xFFFFFFFFu, threadIdx.x >> 5, 0);
     const uint32_t g = lane >> 2, t = lane & 3;
     const uint32_t part = blockIdx.x % P.split;  // rank in the cluster
-    const uint32_t wk = warp & (P.wk - 1u), wr = warp / P.wk, groups = kWarps / P.wk;
-    const uint32_t first = blockIdx.x / P.split * groups * RT;  // the block's first 16-row block
-    const uint32_t b0 = first + wr * RT;
+    const uint32_t b0 = blockIdx.x / P.split * 8;
     const uint32_t e = blockIdx.y;
     uint32_t lo = 0, hi = A.tokens;
     if (A.offsets != nullptr) {
@@ -180,77 +241,134 @@ __global__ void __launch_bounds__(kGvThreads, 2) q4_gemv_kernel(const __grid_con
         hi = uint32_t(min(max(A.offsets[e + 1], int(lo)), int(A.tokens)));
     }
     if (hi == lo) return;  // the same for all blocks of a cluster
+    if (threadIdx.x == 0) {
+        for (uint32_t s = 0; s < Shape::stages; ++s) {
+            mbar_init(&c.full[s], 1 + 32);  // the records, and every lane's copies of x
+            mbar_init(&c.empty[s], kGvWarps);
+        }
+        c.abort = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    __syncthreads();
     const uint8_t* stream = A.stream + e * A.stride;
-    const uint32_t nrec = b0 < L.blocks16 ? min(uint32_t(RT), L.blocks16 - b0) : 0u;
+    const uint32_t h = min(8u, L.blocks16 - b0);
+    const uint32_t s0 = uint32_t(uint64_t(L.slices) * part / P.split);
+    const uint32_t s1 = uint32_t(uint64_t(L.slices) * (part + 1) / P.split);
+    const uint32_t tiles = (hi - lo + 8 * NT - 1) / (8 * NT);
     const Q4Masks mk = Q4Masks::make<HALF>();
-    const uint32_t step = P.split * P.wk;
-    for (uint32_t t0 = lo; t0 < hi; t0 += 8 * NT) {
-        float acc[RT][NT][4] = {};
-        if (nrec > 0) {
-            Slice<RT, NT, PER> v0, v1;
-            uint32_t s = part * P.wk + wk;
-            if (s < L.slices) load_slice(v0, P, stream, b0, s, nrec, t0, hi, g, t);
-            while (s < L.slices) {
-                s += step;
-                if (s < L.slices) load_slice(v1, P, stream, b0, s, nrec, t0, hi, g, t);
-                slice_mma<HALF, RT, NT, PER>(v0, L.half_scales, mk, acc);
-                if (s >= L.slices) break;
-                s += step;
-                if (s < L.slices) load_slice(v0, P, stream, b0, s, nrec, t0, hi, g, t);
-                slice_mma<HALF, RT, NT, PER>(v1, L.half_scales, mk, acc);
-            }
-        }
-        // partial sums of a row group's warps, then of the cluster's blocks, in a fixed order
-#pragma unroll
-        for (int r = 0; r < RT; ++r)
-#pragma unroll
-            for (int n = 0; n < NT; ++n)
-#pragma unroll
-                for (int k = 0; k < 4; ++k)
-                    sums[warp][((r * NT + n) * 4 + k) * 32 + lane] = acc[r][n][k];
-        if (P.split > 1)
-            cg::this_cluster().sync();
-        else
-            __syncthreads();
-        if (part == 0) {
-            for (uint32_t v = threadIdx.x; v < groups * kVals; v += kGvThreads) {
-                // consecutive threads take consecutive rows of one token
-                const uint32_t row = v % (RT * 16), gr = v / (RT * 16) % groups;
-                const uint32_t tok = v / (RT * 16) / groups;
-                const uint32_t r = row >> 4, gg = row & 7u, up = (row >> 3) & 1u;
-                const uint32_t n = tok >> 3, tt = (tok & 7u) >> 1, odd = tok & 1u;
-                const uint32_t at = ((r * NT + n) * 4 + up * 2 + odd) * 32 + gg * 4 + tt;
-                const uint32_t R = (first + gr * RT) * kQ4Rows + row, p = t0 + tok;
-                if (R >= L.rows || p >= hi) continue;
-                float sum = 0.f;
-                for (uint32_t q = 0; q < P.split; ++q) {
-                    const float* from =
-                        P.split > 1 ? cg::this_cluster().map_shared_rank(&sums[0][0], q) : &sums[0][0];
-                    for (uint32_t w = 0; w < P.wk; ++w) sum += from[(gr * P.wk + w) * kVals + at];
+    uint32_t n = 0;  // slices so far
+    bool ok = true;
+    for (uint32_t tile = 0; tile < tiles; ++tile) {
+        const uint32_t t0 = lo + tile * 8 * NT;
+        if (warp == kGvWarps) {  // producer; without a cluster it runs ahead into the next tiles
+            const uint32_t ntok = min(8u * NT, hi - t0);
+            for (uint32_t s = s0; ok && s < s1; ++s) {
+                const uint32_t st = n % Shape::stages, round = n / Shape::stages;
+                ok = round == 0 || gv_wait(&c.empty[st], (round - 1u) & 1u, c, A.status);
+                if (!ok) break;
+                if (lane == 0) {
+                    mbar_arrive_expect_tx(&c.full[st], h * L.rec);
+                    bulk_load(w_ring + st * P.pitch, stream + q4_record(L, b0, s), h * L.rec,
+                              &c.full[st]);
                 }
-                if (A.flags & kQ4Y16) {
-                    uint16_t* y = static_cast<uint16_t*>(A.y) + uint64_t(p) * A.ldy + R;
-                    *y = HALF ? __half_as_ushort(__float2half_rn(sum))
-                              : __bfloat16_as_ushort(__float2bfloat16_rn(sum));
+                __syncwarp();
+                const uint32_t dst = smem_addr(x_ring + st * Shape::x_bytes);
+                if (P.x_bytes == 2) {
+                    gv_copy_x<2>(P, dst, t0, ntok, s, lane);
+                    mbar_arrive(&c.full[st]);
                 } else {
-                    static_cast<float*>(A.y)[uint64_t(p) * A.ldy + R] = sum;
+                    if (P.x_bytes == 16)
+                        gv_copy_x<16>(P, dst, t0, ntok, s, lane);
+                    else if (P.x_bytes == 8)
+                        gv_copy_x<8>(P, dst, t0, ntok, s, lane);
+                    else
+                        gv_copy_x<4>(P, dst, t0, ntok, s, lane);
+                    // this lane's arrival, once its copies have landed
+                    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(
+                                     smem_addr(&c.full[st]))
+                                 : "memory");
                 }
+                ++n;
+            }
+        } else {
+            float acc[NT][4] = {};
+            for (uint32_t s = s0; ok && s < s1; ++s, ++n) {
+                const uint32_t st = n % Shape::stages;
+                ok = gv_wait(&c.full[st], (n / Shape::stages) & 1u, c, A.status);
+                if (!ok) break;
+                if (warp < h)
+                    record_mma<HALF, NT, PER>(smem_addr(w_ring + st * P.pitch) + warp * L.rec,
+                                              smem_addr(x_ring + st * Shape::x_bytes), L.zeros,
+                                              L.half_scales, g, t, mk, acc);
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&c.empty[st]);
+            }
+            if (P.split == 1) {
+#pragma unroll
+                for (int k = 0; k < NT; ++k)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const uint32_t row = (b0 + warp) * kQ4Rows + g + 8 * (j >> 1);
+                        const uint32_t p = t0 + 8 * k + 2 * t + (j & 1);
+                        if (ok && row < L.rows && p < hi) q4_store<HALF>(A, p, row, acc[k][j]);
+                    }
+            } else {
+#pragma unroll
+                for (int k = 0; k < NT; ++k)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        sums[warp * Shape::vals + (k * 4 + j) * 32 + lane] = acc[k][j];
             }
         }
-        if (P.split > 1)
-            cg::this_cluster().sync();
-        else
-            __syncthreads();
+        if (P.split > 1) {
+            // each block adds and writes its share of the rows, over the blocks in order
+            const cg::cluster_group cluster = cg::this_cluster();
+            cluster.sync();
+            for (uint32_t v = part * kGvThreads + threadIdx.x; v < kGvWarps * Shape::vals;
+                 v += P.split * kGvThreads) {
+                const uint32_t r = v / Shape::vals, k = v % Shape::vals / 128, j = v % 128 / 32;
+                const uint32_t gg = v % 32 / 4, tt = v % 4;
+                const uint32_t row = (b0 + r) * kQ4Rows + gg + 8 * (j >> 1);
+                const uint32_t p = t0 + 8 * k + 2 * tt + (j & 1);
+                if (row >= L.rows || p >= hi) continue;
+                float sum = 0.f;
+                for (uint32_t q = 0; q < P.split; ++q) sum += cluster.map_shared_rank(sums, q)[v];
+                q4_store<HALF>(A, p, row, sum);
+            }
+            cluster.sync();
+        }
+    }
+    if (warp == kGvWarps && !ok) {  // let the copies already started land before the block ends
+        asm volatile("cp.async.wait_all;" ::: "memory");
+        for (uint32_t k = n < Shape::stages ? 0 : n - Shape::stages; k < n; ++k)
+            for (int j = 0; j < (1 << 16); ++j)
+                if (gv_poll(&c.full[k % Shape::stages], (k / Shape::stages) & 1u)) break;
     }
     if (blockIdx.x == 0 && threadIdx.x == 0) q4_check_header(stream, L, A.status);
 }
 
-template <bool HALF, int RT, int NT, int PER>
+template <bool HALF, int NT, int PER>
 cudaError_t gv_launch(const GvParams& P, cudaStream_t stream) {
-    const uint32_t rows = kWarps / P.wk * RT;  // records of a block
+    static std::mutex mu;
+    static bool set[64];
+    int dev = 0;
+    cudaError_t err = cudaGetDevice(&dev);
+    if (err != cudaSuccess) return err;
+    if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+    const auto kernel = q4_gemv_kernel<HALF, NT, PER>;
+    {
+        std::lock_guard<std::mutex> lock(mu);
+        if (!set[dev]) {
+            err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       int(gv_smem<NT>(8 * (kQ4Codes + 32 * 4 + 64))));
+            if (err != cudaSuccess) return err;
+            set[dev] = true;
+        }
+    }
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((P.L.blocks16 + rows - 1) / rows * P.split, P.a.experts);
+    cfg.gridDim = dim3((P.L.blocks16 + 7) / 8 * P.split, P.a.experts);
     cfg.blockDim = dim3(kGvThreads);
+    cfg.dynamicSmemBytes = gv_smem<NT>(P.pitch);
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -258,20 +376,14 @@ cudaError_t gv_launch(const GvParams& P, cudaStream_t stream) {
     attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = P.split > 1 ? 1 : 0;
-    return cudaLaunchKernelEx(&cfg, q4_gemv_kernel<HALF, RT, NT, PER>, P);
+    return cudaLaunchKernelEx(&cfg, kernel, P);
 }
 
-template <bool HALF, int RT, int NT>
+template <bool HALF, int NT>
 cudaError_t gv_per(const GvParams& P, cudaStream_t stream) {
-    return P.L.per == 1   ? gv_launch<HALF, RT, NT, 1>(P, stream)
-           : P.L.per == 2 ? gv_launch<HALF, RT, NT, 2>(P, stream)
-                          : gv_launch<HALF, RT, NT, 4>(P, stream);
-}
-
-template <bool HALF>
-cudaError_t gv_tiles(const GvParams& P, int rt, int nt, cudaStream_t stream) {
-    if (rt == 1) return nt == 1 ? gv_per<HALF, 1, 1>(P, stream) : gv_per<HALF, 1, 2>(P, stream);
-    return nt == 1 ? gv_per<HALF, 2, 1>(P, stream) : gv_per<HALF, 2, 2>(P, stream);
+    return P.L.per == 1   ? gv_launch<HALF, NT, 1>(P, stream)
+           : P.L.per == 2 ? gv_launch<HALF, NT, 2>(P, stream)
+                          : gv_launch<HALF, NT, 4>(P, stream);
 }
 
 }  // namespace
@@ -285,30 +397,21 @@ cudaError_t launch_q4_gemv(const Q4GemmArgs& a, const Q4Layout& L, cudaStream_t 
     GvParams P;
     P.a = a;
     P.L = L;
+    P.pitch = 8 * L.rec;
     const uint64_t al = reinterpret_cast<uintptr_t>(a.x) | (a.ldx * 2);
     P.x_bytes = al % 16 == 0 ? 16u : al % 8 == 0 ? 8u : al % 4 == 0 ? 4u : 2u;
-    // Matrices that can have rows, and rows of x a matrix has on average.
+    // Matrices that can have rows, and rows of x such a matrix has on average.
     const uint32_t used = a.offsets == nullptr ? 1u : a.tokens < a.experts ? a.tokens : a.experts;
     const uint32_t rows = (a.tokens + used - 1) / used;
-    const int nt = rows > 8 ? 2 : 1;
-    // Enough blocks to fill the machine first, then long runs of slices for each
-    // warp and two records at a time (x is read once for both).
-    const uint64_t want = 2ull * uint32_t(sms);
-    auto blocks = [&](uint32_t rt, uint32_t wk) {
-        const uint32_t per = kWarps / wk * rt;
-        return uint64_t(used) * ((L.blocks16 + per - 1) / per);
-    };
-    int rt = 2;
-    P.wk = 1;
-    while (P.wk < 8 && (L.slices / P.wk > 4 || blocks(2, P.wk) < want) && P.wk * 2 <= L.slices)
-        P.wk *= 2;
-    if (blocks(2, P.wk) < want) rt = 1;
+    // As many blocks as are resident at a time (two a multiprocessor), if each
+    // then has two slices or more.
+    const uint64_t blocks = uint64_t(used) * ((L.blocks16 + 7) / 8);
     P.split = 1;
-    while (P.split < 8 && blocks(uint32_t(rt), P.wk) * P.split * 2 <= want &&
-           L.slices / (P.wk * P.split) >= 4)
+    while (P.split < 8 && blocks * P.split * 2 <= 2ull * uint32_t(sms) &&
+           L.slices / (2 * P.split) >= 2)
         P.split *= 2;
-    return a.flags & kQ4XHalf ? gv_tiles<true>(P, rt, nt, stream)
-                              : gv_tiles<false>(P, rt, nt, stream);
+    if (a.flags & kQ4XHalf) return rows > 8 ? gv_per<true, 2>(P, stream) : gv_per<true, 1>(P, stream);
+    return rows > 8 ? gv_per<false, 2>(P, stream) : gv_per<false, 1>(P, stream);
 }
 
 }  // namespace wc
