@@ -11,8 +11,13 @@ namespace {
 constexpr uint32_t kStreamFlags = WC_Q4_ZEROS | WC_Q4_SCALES_FP16;
 constexpr uint32_t kAllFlags = kStreamFlags | WC_Q4_X_FP16 | WC_Q4_Y_16BIT;
 
-// Rows of x a matrix up to which wc_q4_gemv.cu is taken.
+// Rows of x a matrix (of experts: on average) up to which wc_q4_gemv.cu is taken.
+// Measured, it and wc_q4_gemm.cu, us: 14336 x 4096, 8 rows 15.7 and 17.3, 16 rows
+// 19.6 and 17.6, 24 rows 34 and 18; 4096 x 14336, 16 rows 17.3 and 17.5; 1024 x
+// 4096, 16 rows 6.8 and 7.8, 24 rows 10.6 and 8.0. Experts (16 of 4096 x 2048),
+// whose rows come unevenly: 8 a matrix 35.5 and 33.3, 16 a matrix 43.7 and 33.9.
 constexpr uint64_t kFewRows = 16;
+constexpr uint64_t kFewRowsExperts = 6;
 
 bool aligned(const void* p, uint32_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1u)) == 0; }
 
@@ -103,8 +108,9 @@ static int q4_product(const void* d_streams, uint64_t stride, uint32_t experts, 
     a.flags = flags;
     a.status = d_status;
     const wc::Q4Layout L = wc::q4_layout(uint32_t(rows), uint32_t(cols), group, flags);
-    const uint64_t mean = d_offsets == nullptr ? tokens : (tokens + experts - 1) / experts;
-    const auto launch = mean <= kFewRows ? wc::launch_q4_gemv : wc::launch_q4_gemm;
+    const bool few = d_offsets == nullptr ? tokens <= kFewRows
+                                          : tokens <= uint64_t(experts) * kFewRowsExperts;
+    const auto launch = few ? wc::launch_q4_gemv : wc::launch_q4_gemm;
     return result(launch(a, L, static_cast<cudaStream_t>(stream)));
 }
 

@@ -760,16 +760,15 @@ __global__ void __launch_bounds__(Roles<NT>::threads, 1)
     __syncthreads();
     tc_fence_after();
     // All 512 columns are this block's, so its tensor memory starts at address 0,
-    // which the roles use as a constant.
-    if (c.tmem_base != 0) {
-        if (tid == 0) report(P.a.status, kStatusTimeout);
-        c.abort = 1;
-    }
+    // which the roles use as a constant (and do nothing, were it ever otherwise).
+    const bool run = c.tmem_base == 0;
+    if (!run && tid == 0) report(P.a.status, kStatusTimeout);
 
     if (warp < kUnpWarp0) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(Roles<NT>::regs_issue));
         if (warp == kWWarp) {
-            if (lane == 0) gm_load_w<NT>(P, S);
+            if (lane == 0 && run) gm_load_w<NT>(P, S);
+        } else if (!run) {
         } else if (warp >= kMWarp0) {
             if (warp == kMWarp0)
                 gm_mma<NT, HALF, PER, 0>(P, S);
@@ -789,12 +788,12 @@ __global__ void __launch_bounds__(Roles<NT>::threads, 1)
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(Roles<NT>::regs));
     } else if (warp < Roles<NT>::scl_warp0) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(Roles<NT>::regs_unpack));
-        gm_unpack<NT, HALF, PER>(P, S, warp - kUnpWarp0, lane);
+        if (run) gm_unpack<NT, HALF, PER>(P, S, warp - kUnpWarp0, lane);
         __syncthreads();
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(Roles<NT>::regs));
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(Roles<NT>::regs_scale));
-        gm_scale<NT, HALF, PER>(P, S, warp - Roles<NT>::scl_warp0, lane);
+        if (run) gm_scale<NT, HALF, PER>(P, S, warp - Roles<NT>::scl_warp0, lane);
         __syncthreads();
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(Roles<NT>::regs));
     }

@@ -222,6 +222,71 @@ def test_experts(wclib, cuda, counts, rows, cols, group, zeros, half):
         assert torch.equal(y, y2)
 
 
+@pytest.mark.parametrize("rows,cols", [(200, 2056), (1000, 130)])
+@pytest.mark.parametrize("crowd", [5, 40, 90])
+def test_one_crowded_expert_among_many(wclib, cuda, rows, cols, crowd):
+    """Few rows an expert on average, many at one: several tiles of rows of x
+    against the same matrix, in the product of few rows (up to 6 an expert) and
+    in the other; the first and last experts empty."""
+    E = 16
+    rng, m, Ws = experts_case(wclib, cuda, E, rows, cols, 64, True, False, rows + crowd)
+    counts = [0, 0, 1, crowd] + [0] * 10 + [2, 0]
+    offsets = np.concatenate([[0], np.cumsum(counts)]).astype(np.int32)
+    x, xd = acts(rng, sum(counts), cols, False, cuda)
+    status = torch.zeros(1, dtype=torch.int32, device=cuda)
+    y = wclib.gemm_q4_experts(m, x, dev(offsets, cuda), status=status)
+    assert status.item() == 0
+    for e in range(E):
+        a, b = offsets[e], offsets[e + 1]
+        if b > a:
+            check(y[a:b], Ws[e], xd[a:b], 64, cols)
+    assert torch.equal(y, wclib.gemm_q4_experts(m, x, dev(offsets, cuda)))
+
+
+def test_every_alignment_of_rows_of_x(wclib, cuda):
+    """Rows of x at every multiple of 2 bytes from a 16-byte boundary, dense and
+    odd lengths, few rows and many: the same bits as from an aligned copy."""
+    rng = np.random.default_rng(77)
+    m, W = matrix(wclib, rng, 150, 333, 32, True, True, cuda)
+    for tokens in (5, 70):
+        x, xd = acts(rng, tokens, 333, True, cuda)
+        wide = torch.zeros((tokens, 336), dtype=x.dtype, device=cuda)
+        wide[:, :333] = x
+        ref = wclib.gemm_q4(m, wide[:, :333])
+        check(ref, W, xd, 32, 333)
+        for at in range(8):
+            for pad in (334, 336, 340, 341):
+                buf = torch.full((tokens * pad + 16,), float("nan"), dtype=x.dtype, device=cuda)
+                v = buf[at:at + tokens * pad].view(tokens, pad)[:, :333]
+                v.copy_(x)
+                assert torch.equal(wclib.gemm_q4(m, v), ref), (tokens, at, pad)
+
+
+def test_calls_from_two_threads(wclib, cuda):
+    """Two host threads, each on its own stream, many calls at once."""
+    import threading
+    rng = np.random.default_rng(78)
+    m, W = matrix(wclib, rng, 300, 640, 64, False, False, cuda)
+    xs = [acts(rng, t, 640, False, cuda)[0] for t in (3, 40)]
+    want = [wclib.gemm_q4(m, x) for x in xs]
+    torch.cuda.synchronize()
+    bad = []
+
+    def work(k):
+        s = torch.cuda.Stream()
+        for _ in range(50):
+            y = wclib.gemm_q4(m, xs[k], stream=s)
+            s.synchronize()
+            if not torch.equal(y, want[k]):
+                bad.append(k)
+    threads = [threading.Thread(target=work, args=(k,)) for k in (0, 1)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not bad
+
+
 def test_experts_with_wild_offsets_stay_inside(wclib, cuda):
     """Offsets outside the matrices are clamped: no row outside x and y is touched."""
     rng, m, Ws = experts_case(wclib, cuda, 3, 64, 256, 64, False, False, 5)
