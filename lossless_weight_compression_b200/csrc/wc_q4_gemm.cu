@@ -26,6 +26,20 @@
 // With few units, the blocks of a cluster share a unit's slices and add their
 // sums through distributed shared memory in a fixed order: y is the same on
 // every run. Every wait is bounded by the device timer.
+//
+// Measured (GPU time, BF16; beside it the larger of the bytes at the copy's rate
+// and the operations at the matrix product's): 64 rows of x through 14336 x 4096,
+// groups of 128, 19 us (5.1); 512 rows through 4096 x 14336, groups of 64 with zero
+// points, 69 us (35), 0.87 PFLOP/s; 2000 rows over 8 experts of 14336 x 4096, groups
+// of 128 with zero points, 258 us (137), 0.91 PFLOP/s. Bound by instruction issue
+// (0.69 a cycle and scheduler at 512 rows, of which a third is useful arithmetic,
+// the rest waits, addresses and moves around it) and, for groups of 64 and less,
+// by an accumulator's round trip of some 1000 cycles (multiply, commit, read,
+// hand back) with two of them; the tensor pipe is busy 34 % of the time. Steps on
+// the way (512 rows): one issuing thread, 8 + 8 warps 135 us; two issuing warps 104;
+// no time limits inside polls, uniform issuing 91; one barrier a group 77; sums by
+// 16 warps, pairs scaled where they were read 73; barrier addresses kept in
+// registers 68.
 #include <cooperative_groups.h>
 #include <stddef.h>
 #include <string.h>
@@ -66,8 +80,8 @@ struct Roles {
     static constexpr int threads = 32 * warps;
     // Registers of a thread at launch and after the roles split.
     static constexpr int regs = NT == 128 ? 72 : 80;
-    static constexpr int regs_issue = NT == 128 ? 56 : 64, regs_unpack = regs_issue;
-    static constexpr int regs_scale = NT == 128 ? 80 : 104;
+    static constexpr int regs_issue = NT == 128 ? 48 : 64, regs_unpack = regs_issue;
+    static constexpr int regs_scale = NT == 128 ? 88 : 104;
     static_assert(threads * regs <= 65536, "registers at launch");
     static_assert(4 * regs_issue + 4 * unp_turns * regs_unpack + scl_warps * regs_scale <=
                       warps * regs,
@@ -440,9 +454,10 @@ __device__ void gm_unpack(const GmParams& P, const GmSmem& S, int wi, int lane) 
             !gm_wait_warp(WC_BAR(s_free) + 8u * (st), (n / kSRing - 1u) & 1u, c, P.a.status))
             return;
         tc_fence_after();
-        // not unrolled: the roles share an instruction cache
+        // Stores of four registers as soon as they are there: with 16 a store the
+        // warps stood still (83 against 68 us, 512 rows of x through 4096 x 14336).
         uint32_t src = row_at + ws * kWStage, dst = t_lane + st * 64u;
-#pragma unroll 1
+#pragma unroll 2
         for (int k = 0; k < 4; ++k, src += 256u, dst += 4u) {
             const uint4 v = lds128(src);
 #pragma unroll
