@@ -5,9 +5,9 @@
 // All but the sort move each row once: a token's row is read once and written to
 // its slots' rows, or its slots' rows are read and summed, with 16-byte accesses
 // where the rows allow them. Measured (BF16; beside it the bytes at the copy's
-// rate): 16,384 tokens x 6 slots of 4 KB rows, 5 % dropped: gather 72 us (69),
-// its gradient 75 us (67), sort 22 us; 8192 tokens x 2 slots of 8 KB rows: combine
-// and its backward together 98 us (83).
+// rate): 16,384 tokens x 6 slots of 4 KB rows: gather 76 us (73), its gradient 79
+// us (73), sort 19 us; 8192 tokens x 2 slots of 8 KB rows: combine 40 us (31), its
+// backward 56 us (52).
 #include <cooperative_groups.h>
 
 #include <mutex>
@@ -28,7 +28,7 @@ namespace cg = cooperative_groups;
 // warps, the cluster's blocks (through distributed shared memory) and the
 // experts; then each warp adds the sums to its slots' ranks. No workspace and one
 // launch. The counting is bound by instruction issue on the cluster's eight
-// multiprocessors (98,304 slots: 22 us), far below the row copies that follow.
+// multiprocessors (98,304 slots: 19 us), far below the row copies that follow.
 // ---------------------------------------------------------------------------
 constexpr int kSortThreads = 1024;
 constexpr int kSortWarps = kSortThreads / 32;

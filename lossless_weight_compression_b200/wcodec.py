@@ -867,7 +867,8 @@ class Q4Matrix:
 
 def _q4_buffer(m: Q4Matrix, dims: int) -> torch.Tensor:
     b = m.buffer
-    if b.dtype != torch.uint8 or b.dim() != dims or (b.shape[-1] > 1 and b.stride(-1) != 1):
+    if b.dtype != torch.uint8 or b.dim() != dims or not (
+            b.is_contiguous() or b.shape[-1] <= 1 or b.stride(-1) == 1):
         raise ValueError("a 4-bit stream is a dense uint8 tensor of %d dimension(s); got %s %s"
                          % (dims, b.dtype, tuple(b.shape)))
     return b
