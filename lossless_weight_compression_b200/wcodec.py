@@ -14,6 +14,7 @@ from __future__ import annotations
 
 import contextlib
 import ctypes
+import functools
 import os
 from dataclasses import dataclass
 
@@ -874,6 +875,7 @@ def _q4_buffer(m: Q4Matrix, dims: int) -> torch.Tensor:
     return b
 
 
+@functools.lru_cache(maxsize=256)
 def _q4_size(rows: int, cols: int, group: int, flags: int) -> int:
     size = wc_q4_bytes(rows, cols, group, flags) if rows >= 0 and cols >= 0 else 0
     if size == 0:

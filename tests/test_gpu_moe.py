@@ -207,6 +207,27 @@ def test_wild_inverse_names_no_row(wclib, cuda):
     assert dw.tolist() == [[128.0, 0.0], [0.0, 0.0]]
 
 
+def test_rows_past_32_bits(wclib, cuda):
+    """Sorted rows of more than 2^32 elements: copied, summed and their gradients."""
+    tokens, top, cols = 140000, 4, 8192
+    ids = torch.randint(0, 64, (tokens, top), device=cuda).to(torch.int32)
+    plan = wclib.moe_sort(ids, 64)
+    x = torch.randn((tokens, cols), device=cuda, dtype=torch.bfloat16)
+    rows = wclib.moe_gather(x, plan)
+    for a in (0, tokens * top - 500):
+        assert torch.equal(rows[a:a + 500], x[(plan.order[a:a + 500] // top).long()])
+    out = wclib.moe_combine(rows, plan, None)
+    assert torch.equal(out, x * 4)  # four equal terms: exact
+    del out
+    w = torch.full((tokens, top), 2.0, device=cuda)
+    drows, dw = wclib.moe_combine_backward(x, rows, plan, w)
+    assert torch.equal(drows[-500:], rows[-500:] * 2) and torch.equal(drows[:500], rows[:500] * 2)
+    ref = x[-50:].double().square().sum(1, keepdim=True).expand(50, top)
+    assert ((dw[-50:].double() - ref).abs() <= (cols + 16) * 2.0 ** -24 * ref).all()
+    del rows, drows
+    torch.cuda.empty_cache()
+
+
 def quantized_experts(wc, E, rows, cols, group, device, seed):
     g = torch.Generator(device="cpu").manual_seed(seed)
     ms = [wc.quantize_q4((torch.randn((rows, cols), generator=g) * 0.05).to(device, torch.bfloat16), group)

@@ -262,6 +262,66 @@ def test_every_alignment_of_rows_of_x(wclib, cuda):
                 assert torch.equal(wclib.gemm_q4(m, v), ref), (tokens, at, pad)
 
 
+@pytest.mark.parametrize("cols", [1, 2, 3, 8, 16, 31, 64, 127])
+def test_narrow_matrices(wclib, cuda, cols):
+    """Matrices of less than a slice, in one row of x and many, aligned and not."""
+    rng = np.random.default_rng(cols)
+    for rows in (1, 17, 129):
+        m, W = matrix(wclib, rng, rows, cols, 32, bool(rows % 2), False, cuda)
+        for tokens in (1, 9, 20, 130):
+            x, xd = acts(rng, tokens, cols, False, cuda)
+            check(wclib.gemm_q4(m, x), W, xd, 32, cols)
+
+
+def test_no_expert_has_rows(wclib, cuda):
+    """Offsets all equal, with few rows of x and with many: nothing is written."""
+    rng, m, _ = experts_case(wclib, cuda, 4, 64, 256, 64, False, False, 6)
+    for tokens in (3, 100):
+        x, _ = acts(rng, tokens, 256, False, cuda)
+        for at in (0, 2, tokens):
+            y = torch.full((tokens, 64), 7.0, device=cuda)
+            off = torch.full((5,), at, dtype=torch.int32, device=cuda)
+            wclib.gemm_q4_experts(m, x, off, y=y)
+            assert (y == 7).all()
+
+
+def test_many_experts_of_both_products(wclib, cuda):
+    """1024 experts (the most), some empty, in the product of few rows and the other."""
+    rng = np.random.default_rng(12)
+    q, s, z = q4_plain.make(rng, 16, 128, 128, False, False)
+    one = dev(q4_plain.stream(q, s, z, 128, False), cuda)
+    W = q4_plain.weights(q, s, z, 128, False)
+    m = wclib.Q4Matrix(one.repeat(1024, 1).contiguous(), 16, 128, 128, False, torch.bfloat16)
+    for most in (3, 20):
+        counts = rng.integers(0, most, 1024)
+        offsets = np.concatenate([[0], np.cumsum(counts)]).astype(np.int32)
+        x, xd = acts(rng, int(offsets[-1]), 128, False, cuda)
+        check(wclib.gemm_q4_experts(m, x, dev(offsets, cuda)), W, xd, 128, 128)
+
+
+def test_offsets_past_32_bits(wclib, cuda):
+    """A matrix of more than 2^32 elements: its last rows are those of a matrix of
+    their own, quantized, expanded and multiplied (few rows of x and many)."""
+    rows, cols, tail = 524288 + 256, 8192, 256
+    w = torch.empty((rows, cols), dtype=torch.bfloat16, device=cuda)
+    for k in range(0, rows, 65536):
+        w[k:k + 65536].normal_()
+    m = wclib.quantize_q4(w, 128)
+    last = wclib.quantize_q4(w[-tail:], 128)
+    assert torch.equal(m.buffer[128 - last.buffer.numel():], last.buffer[128:])
+    w.zero_()
+    wclib.dequantize_q4(m, out=w)
+    assert torch.equal(w[-tail:], wclib.dequantize_q4(last))
+    del w
+    for tokens in (2, 40):
+        x = torch.randn((tokens, cols), device=cuda).to(torch.bfloat16)
+        y = wclib.gemm_q4(m, x)[:, -tail:].double()
+        W = wclib.dequantize_q4(last, torch.float32).double()
+        tol = (128 + 64 + 64) * 2.0 ** -22 * (x.double().abs() @ W.abs().T)
+        assert ((y - x.double() @ W.T).abs() <= tol).all()
+    torch.cuda.empty_cache()
+
+
 def test_calls_from_two_threads(wclib, cuda):
     """Two host threads, each on its own stream, many calls at once."""
     import threading
