@@ -480,14 +480,16 @@ int wc_decompress_tans_batch(const wc_batch_item *h_items, uint32_t count, int32
  *  wc_q4_quantize    rounds rows x cols 16-bit weights (rows ld elements apart,
  *                    2-byte aligned; BF16, or FP16 with WC_Q4_SCALES_FP16: the
  *                    scales have the weights' type) to a stream at d_out. Per
- *                    row and group, to nearest even (ranges in FP32):
+ *                    row and group, to nearest even (ranges and scales in FP32
+ *                    before round16):
  *                      s = round16(max|w| / 7), q = clamp(rint(w/s), -8, 7) + 8
  *                    or, with WC_Q4_ZEROS, lo = min(w, 0), hi = max(w, 0),
  *                      s = round16((hi - lo) / 15), z = clamp(rint(-lo/s), 0, 15),
  *                      q = clamp(rint(w/s) + z, 0, 15)
  *                    s = 0: every code stands for zero. A NaN in a group, or
  *                    infinities of both signs, makes its scale NaN; other
- *                    infinities make it infinite.
+ *                    infinities make it infinite, and so does (with zero
+ *                    points) a range of finite weights that FP32 cannot hold.
  *  wc_q4_pack        the stream of given codes (u8, rows x cols, low 4 bits
  *                    used), scales (u16, rows x groups) and zero points (u8,
  *                    rows x groups; with WC_Q4_ZEROS, else NULL), all dense:

@@ -213,10 +213,12 @@ __global__ void __launch_bounds__(kQ4Threads)
             const float inf = __int_as_float(0x7F800000);
             float range = ZEROS ? hi + lo : fmaxf(hi, lo);
             if (hi != hi || (hi == inf && lo == inf)) range = __int_as_float(0x7FC00000);
-            // range / steps, again by a Newton step on the remainder
+            // range / steps, again by a Newton step on the remainder: the nearest FP32
+            // value of the quotient, which lies 1/14 (1/30) of a step or more from the
+            // middle of two. Infinities and NaN, whose remainder is NaN, stay as they are.
             const float t0 = range * kInv;
             const float t1 = fmaf(fmaf(-t0, kSteps, range), kInv, t0);
-            const uint16_t sbits = from_float<HALF>(range < 3e38f ? t1 : range);
+            const uint16_t sbits = from_float<HALF>(range < inf ? t1 : range);
             const float sc = to_float<HALF>(sbits);
             uint32_t word;
             float z = 8.f;

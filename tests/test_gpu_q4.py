@@ -438,3 +438,76 @@ def test_quantized_layer_matches_its_dequantized_weights(wclib, cuda):
             ref, absum = x.double() @ W.T, x.double().abs() @ W.abs().T
             y = wclib.gemm_q4(m, x)
             assert ((y.double() - ref).abs() <= (group + 4096 // group + 64) * 2.0 ** -22 * absum).all()
+
+
+def plain_quantize_fp32_ranges(w, group, zeros, dtype):
+    """plain_quantize with a group's range and the range's quotient in FP32, as
+    the definition has them (w float64 of finite values): a range of both signs
+    may be rounded there, or be infinite."""
+    rows, cols = w.shape
+    g = q4_plain.groups_of(cols, group)
+    S, Z, Q = np.zeros((rows, g)), np.zeros((rows, g)), np.zeros((rows, cols))
+    for k in range(g):
+        p = w[:, k * group:(k + 1) * group]
+        lo, hi = np.minimum(p.min(1), 0), np.maximum(p.max(1), 0)
+        with np.errstate(over="ignore"):
+            span = hi.astype(np.float32) - lo.astype(np.float32) if zeros else np.maximum(hi, -lo).astype(np.float32)
+            s = torch.from_numpy(span / np.float32(15 if zeros else 7)).to(dtype).double().numpy()
+        d = np.where(s > 0, s, 1)
+        z = np.clip(np.rint(-lo / d), 0, 15) if zeros else np.full(rows, 8.0)
+        z = np.where(s > 0, z, 0.0 if zeros else 8.0)
+        q = np.clip(np.rint(p / d[:, None]) + z[:, None], 0, 15)
+        S[:, k], Z[:, k] = s, z
+        Q[:, k * group:(k + 1) * group] = np.where(s[:, None] > 0, q, z[:, None])
+    bits = torch.from_numpy(S).to(dtype).view(torch.int16).numpy().view(np.uint16)
+    return Q.astype(np.uint8), bits, Z.astype(np.uint8) if zeros else None
+
+
+# Largest magnitudes of a row's groups: the largest finite values, scales on both sides of 1e30 and
+# 1e-30 (where the kernel changes its way to a quotient), subnormal scales, scales that round to 0.
+MAGNITUDES = {
+    False: [3.39e38, 3.2e38, 3.0e38, 2.99e38, 1e37, 1.6e31, 7.1e30, 6.9e30, 1e30, 7.1e-30, 6.9e-30, 1e-32, 8e-38,
+            1e-38, 1e-39, 9e-41, 3e-40],
+    True: [65504.0, 65000.0, 30.0, 1e-4, 6e-5, 4e-5, 3e-6, 5e-7, 2e-7, 6e-8],
+}
+
+
+@pytest.mark.parametrize("zeros", [False, True])
+@pytest.mark.parametrize("half", [False, True])
+@pytest.mark.parametrize("group", [32, 128])
+def test_quantize_over_the_whole_range_of_the_type(wclib, cuda, group, half, zeros):
+    """Groups whose scale is among the type's largest or smallest, of both signs
+    and of one, byte for byte; half steps among the values (ties to even)."""
+    rng = np.random.default_rng(group + half)
+    cols = 300
+    rows = []
+    for mag in MAGNITUDES[half]:
+        for kind in range(4):
+            u = rng.uniform(-1, 1, cols)
+            if kind == 1:
+                u = np.abs(u)
+            elif kind == 2:
+                u = -np.abs(u)
+            elif kind == 3:  # halves of a fourteenth (of a thirtieth) of the range
+                u = rng.integers(-14, 15, cols) / (30 if zeros else 14)
+            u[::group] = -1.0 if kind == 2 else 1.0  # each group's largest magnitude
+            if kind == 0:
+                u[1::group] = -0.5
+            rows.append(u * mag)
+    w = torch.from_numpy(np.stack(rows)).float().to(DT[half])
+    assert w.isfinite().all()
+    q, s, z = plain_quantize_fp32_ranges(w.double().numpy(), group, zeros, DT[half])
+    got = wclib.quantize_q4(w.to(cuda), group, zeros=zeros).buffer.cpu().numpy()
+    assert np.array_equal(got, q4_plain.stream(q, s, z, group, half))
+
+
+def test_quantize_finite_weights_whose_range_is_infinite(wclib, cuda):
+    """With zero points a range of both signs can pass FP32: the scale is then
+    infinite, as the definition's FP32 range is. Without them it cannot."""
+    w = torch.full((16, 128), 3e38, dtype=torch.bfloat16)
+    w[:, ::2] = -3e38
+    for zeros in (False, True):
+        q, s, z = plain_quantize_fp32_ranges(w.double().numpy(), 128, zeros, torch.bfloat16)
+        got = wclib.quantize_q4(w.to(cuda), 128, zeros=zeros).buffer.cpu().numpy()
+        assert np.array_equal(got, q4_plain.stream(q, s, z, 128, False))
+        assert np.isinf(q4_plain.scale_values(s, False)).all() == zeros
