@@ -1016,17 +1016,20 @@ def gemm_q4_experts(m: Q4Matrix, x: torch.Tensor, offsets: torch.Tensor, *,
                     status: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """gemm_q4 over the matrices of m.buffer's experts: rows offsets[e] ..
     offsets[e + 1] - 1 of x take matrix e (offsets int32, as moe_sort gives
-    them). Rows outside every range are left as they were in ``y``."""
+    them). The streams may lie apart, each a multiple of 16 bytes from the last. Rows outside every range are left as they were in ``y``."""
     b = _q4_buffer(m, 2)
     experts, size = b.shape
     _vector(offsets, (experts + 1,), torch.int32, "offsets", b.device)
     tokens, ldx, ldy, flags, out_dtype = _q4_product_args(m, b, x, y, out_dtype)
+    need = _q4_size(m.rows, m.cols, m.group, m.flags())
+    if size < need:  # (the stride between streams says nothing of the last one's length)
+        raise WcodecError(WC_ERR_CORRUPT_STREAM, "streams of %d bytes each; one takes %d" % (size, need))
     if not _here(b, stream):
         with _there(b.device, stream):
             return gemm_q4_experts(m, x, offsets, y=y, out_dtype=out_dtype, status=status)
     if y is None:
         y = x.new_empty((tokens, m.rows), dtype=out_dtype)
-    rc = lib().wc_q4_gemm_experts(b.data_ptr(), b.stride(0) if experts > 1 else size, experts,
+    rc = lib().wc_q4_gemm_experts(b.data_ptr(), b.stride(0) if experts > 1 else need, experts,
                                   m.rows, m.cols, m.group, flags, x.data_ptr(), ldx, tokens,
                                   offsets.data_ptr(), y.data_ptr(), ldy,
                                   None if status is None else _status_ptr(status, b.device),

@@ -511,3 +511,24 @@ def test_quantize_finite_weights_whose_range_is_infinite(wclib, cuda):
         got = wclib.quantize_q4(w.to(cuda), 128, zeros=zeros).buffer.cpu().numpy()
         assert np.array_equal(got, q4_plain.stream(q, s, z, 128, False))
         assert np.isinf(q4_plain.scale_values(s, False)).all() == zeros
+
+
+def test_streams_of_experts_in_a_wider_buffer(wclib, cuda):
+    """Streams that lie apart in a buffer of more columns, and one expert's with
+    a few bytes behind it: the same bits as from a stack of their own."""
+    rng, m, Ws = experts_case(wclib, cuda, 3, 64, 256, 64, False, False, 8)
+    size = wclib.wc_q4_bytes(64, 256, 64, 0)
+    own = m.buffer[:, :size].contiguous()
+    wide = torch.zeros((3, size + 96), dtype=torch.uint8, device=cuda)
+    wide[:, 32:32 + size] = own
+    off = torch.tensor([0, 5, 5, 12], dtype=torch.int32, device=cuda)
+    x, xd = acts(rng, 12, 256, False, cuda)
+
+    def call(b, o):
+        return wclib.gemm_q4_experts(wclib.Q4Matrix(b, 64, 256, 64, False, torch.bfloat16), x[:int(o[-1])], o)
+    y = call(own, off)
+    check(y[:5], Ws[0], xd[:5], 64, 256)
+    check(y[5:], Ws[2], xd[5:], 64, 256)
+    assert torch.equal(call(wide[:, 32:32 + size], off), y)
+    assert torch.equal(call(wide[:, 32:], off), y)
+    assert torch.equal(call(wide[:1, 32:32 + size + 8], off[:2]), y[:5])

@@ -142,3 +142,23 @@ def test_helpers_refuse_host_tensors_and_wrong_shapes(wclib):
     with pytest.raises(ValueError, match="dense rows"):
         wclib.moe_combine_backward(torch.zeros((1, 8), dtype=torch.bfloat16).expand(4, 8), w, plan,
                                    None)
+
+
+def test_experts_streams_shorter_than_their_stride(wclib):
+    """Views of a stack whose rows are too short for a stream, however far apart
+    they lie, are refused as a short stream of one matrix is; views that hold
+    their streams pass (and are then refused for lying on the host)."""
+    size = wclib.wc_q4_bytes(32, 256, 128, 0)
+    big = torch.zeros((4, size + 64), dtype=torch.uint8)
+    x, off = torch.zeros((4, 256), dtype=torch.bfloat16), torch.zeros(5, dtype=torch.int32)
+
+    def call(b):
+        return wclib.gemm_q4_experts(wclib.Q4Matrix(b, 32, 256, 128, False, torch.bfloat16), x,
+                                     off[:b.shape[0] + 1])
+    for short in (big[:, 80:], big[:, :size - 1], big[:, :0], big[:1, :size - 1], big[2:, 65:]):
+        with pytest.raises(wclib.WcodecError) as e:
+            call(short)
+        assert e.value.status == wclib.WC_ERR_CORRUPT_STREAM
+    for whole in (big, big[:, 64:], big[:, :size], big[:1, :size + 8]):
+        with pytest.raises(ValueError, match="CUDA"):
+            call(whole)
