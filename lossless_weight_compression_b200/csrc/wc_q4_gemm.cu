@@ -45,6 +45,7 @@
 #include <string.h>
 
 #include "wc_q4_core.cuh"
+#include "wc_ring.cuh"
 #include "wc_tcgen05.cuh"
 
 namespace wc {
@@ -260,7 +261,7 @@ struct Ring {
     __device__ __forceinline__ void next() {
         if (++s == N) s = 0, ++round;
     }
-    __device__ __forceinline__ uint32_t full() const { return round & 1u; }
+    __device__ __forceinline__ uint32_t fills() const { return round * N + s; }
     __device__ __forceinline__ uint32_t empty() const { return (round - 1u) & 1u; }
 };
 
@@ -271,8 +272,10 @@ __device__ __forceinline__ void my_slices(const GmParams& P, uint32_t& s0, uint3
     s1 = uint32_t(uint64_t(P.L.slices) * (r + 1) / P.split);
 }
 
+// The loading roles return how many copies they started: those that may still be in
+// flight when the roles end are waited for (gm_drain) if one of them gave up.
 template <int NT>
-__device__ void gm_load_w(const GmParams& P, const GmSmem& S) {
+__device__ uint32_t gm_load_w(const GmParams& P, const GmSmem& S) {
     GmCtl& c = *S.ctl;
     const uint32_t cb = ctl_base(S);
     const Q4Layout& L = P.L;
@@ -297,16 +300,11 @@ __device__ void gm_load_w(const GmParams& P, const GmSmem& S) {
                       &c.w_full[w.s]);
         }
     }
-    if (!ok) {  // let the copies already started land before the block ends
-        for (uint32_t k = 0; k < kWRing; ++k) {
-            const uint32_t r = k < w.s ? w.round : w.round - 1u;
-            if (k < w.s || w.round > 0) mbar_wait(&c.w_full[k], r & 1u, nullptr);
-        }
-    }
+    return w.fills();
 }
 
 template <int NT, int PER>
-__device__ void gm_load_x_tma(const GmParams& P, const GmSmem& S) {
+__device__ uint32_t gm_load_x_tma(const GmParams& P, const GmSmem& S) {
     GmCtl& c = *S.ctl;
     const uint32_t cb = ctl_base(S);
     uint32_t s0, s1, e = 0;
@@ -331,15 +329,22 @@ __device__ void gm_load_x_tma(const GmParams& P, const GmSmem& S) {
             tma_load_2d(d + NT * 128, &P.x_map, int32_t(s * kQ4Cols + 64), int32_t(t.tok0), b1);
         }
     }
-    if (!ok) {  // (bounded: an aborted slice's other arrivals may never come)
-        for (uint32_t k = 0; k < kSRing; ++k) {
-            const uint32_t r = k < x.s ? x.round : x.round - 1u;
-            if (k < x.s || x.round > 0) {
-                mbar_wait(&c.g_full[k][0], r & 1u, nullptr);
-                mbar_wait(&c.g_full[k][PER / 2], r & 1u, nullptr);
-            }
-        }
-    }
+    return x.fills();
+}
+
+// No copy outlives the block: its shared memory goes to another. After an abort the
+// other arrivals of a slice may never come; the first wait that runs out has given
+// all copies its time.
+template <int PER>
+__device__ void gm_drain(GmCtl& c, uint32_t w_fills, uint32_t x_fills) {
+    bool landed = true;
+    ring_last_fills(w_fills, kWRing, [&](uint32_t st, uint32_t parity) {
+        landed = landed && mbar_wait(&c.w_full[st], parity, nullptr);
+    });
+    ring_last_fills(x_fills, kSRing, [&](uint32_t st, uint32_t parity) {
+        landed = landed && mbar_wait(&c.g_full[st][0], parity, nullptr) &&
+                 mbar_wait(&c.g_full[st][PER / 2], parity, nullptr);
+    });
 }
 
 // Rows of x that TMA cannot take: V-byte copies (V = 8, 4: cp.async; 2: through
@@ -781,8 +786,9 @@ __global__ void __launch_bounds__(Roles<NT>::threads, 1)
 
     if (warp < kUnpWarp0) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(Roles<NT>::regs_issue));
+        uint32_t w_fills = 0, x_fills = 0;
         if (warp == kWWarp) {
-            if (lane == 0 && run) gm_load_w<NT>(P, S);
+            if (lane == 0 && run) w_fills = gm_load_w<NT>(P, S);
         } else if (!run) {
         } else if (warp >= kMWarp0) {
             if (warp == kMWarp0)
@@ -790,7 +796,7 @@ __global__ void __launch_bounds__(Roles<NT>::threads, 1)
             else
                 gm_mma<NT, HALF, PER, 1>(P, S);
         } else if (P.x_bytes == 16) {
-            if (lane == 0) gm_load_x_tma<NT, PER>(P, S);
+            if (lane == 0) x_fills = gm_load_x_tma<NT, PER>(P, S);
         } else if (P.x_bytes == 8) {
             gm_load_x_any<NT, PER, 8>(P, S, lane);
         } else if (P.x_bytes == 4) {
@@ -800,6 +806,8 @@ __global__ void __launch_bounds__(Roles<NT>::threads, 1)
         }
         __syncwarp();     // (of roles that one lane takes)
         __syncthreads();  // (no warp spins for the registers that the scaling warps hold)
+        if (w_fills + x_fills > 0 && c.abort) gm_drain<PER>(c, w_fills, x_fills);
+        __syncwarp();
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(Roles<NT>::regs));
     } else if (warp < Roles<NT>::scl_warp0) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(Roles<NT>::regs_unpack));

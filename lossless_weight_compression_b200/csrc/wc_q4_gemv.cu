@@ -30,6 +30,7 @@
 #include <mutex>
 
 #include "wc_q4_core.cuh"
+#include "wc_ring.cuh"
 
 namespace wc {
 namespace {
@@ -338,11 +339,15 @@ __global__ void __launch_bounds__(kGvThreads, 2) q4_gemv_kernel(const __grid_con
             cluster.sync();
         }
     }
-    if (warp == kGvWarps && !ok) {  // let the copies already started land before the block ends
+    // No copy outlives the block, whichever warp gave up (bounded polls). Where none
+    // did, the warps have waited for every copy.
+    __syncthreads();
+    if (warp == kGvWarps && c.abort) {
         asm volatile("cp.async.wait_all;" ::: "memory");
-        for (uint32_t k = n < Shape::stages ? 0 : n - Shape::stages; k < n; ++k)
+        ring_last_fills(n, Shape::stages, [&](uint32_t st, uint32_t parity) {
             for (int j = 0; j < (1 << 16); ++j)
-                if (gv_poll(&c.full[k % Shape::stages], (k / Shape::stages) & 1u)) break;
+                if (__all_sync(0xFFFFFFFFu, gv_poll(&c.full[st], parity))) break;
+        });
     }
     if (blockIdx.x == 0 && threadIdx.x == 0) q4_check_header(stream, L, A.status);
 }
