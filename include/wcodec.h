@@ -513,9 +513,11 @@ int wc_decompress_tans_batch(const wc_batch_item *h_items, uint32_t count, int32
  *                    bounds the rows of x and y; offsets are clamped to it, and
  *                    rows outside every range are neither read nor written.
  * The expanding calls check the header on the device (WC_ERR_CORRUPT_STREAM in
- * *d_status; the output is then unspecified); a stream shorter than its size
- * returns WC_ERR_CORRUPT_STREAM without launching. Nothing is read outside the
- * stated buffers whatever they hold.
+ * *d_status; the output is then unspecified); of experts' streams, those whose
+ * expert has rows. A product whose waits ran out (WC_ERR_TIMEOUT) leaves what it
+ * did not finish as it was or NaN, never as partial sums. A stream shorter than
+ * its size returns WC_ERR_CORRUPT_STREAM without launching. Nothing is read
+ * outside the stated buffers whatever they hold.
  */
 #define WC_Q4_ZEROS 1u
 #define WC_Q4_SCALES_FP16 2u

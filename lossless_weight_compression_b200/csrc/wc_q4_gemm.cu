@@ -782,7 +782,10 @@ __global__ void __launch_bounds__(Roles<NT>::threads, 1)
     // All 512 columns are this block's, so its tensor memory starts at address 0,
     // which the roles use as a constant (and do nothing, were it ever otherwise).
     const bool run = c.tmem_base == 0;
-    if (!run && tid == 0) report(P.a.status, kStatusTimeout);
+    if (!run && tid == 0) {
+        report(P.a.status, kStatusTimeout);
+        c.abort = 1;
+    }
 
     if (warp < kUnpWarp0) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(Roles<NT>::regs_issue));
@@ -822,6 +825,12 @@ __global__ void __launch_bounds__(Roles<NT>::threads, 1)
     }
     __syncwarp();
     if (P.split > 1) {
+        if (c.abort) {  // (the roles have ended: the same for all threads)
+            __syncthreads();  // the last copies into this memory have landed
+            float* red = reinterpret_cast<float*>(S.x);
+            for (uint32_t k = tid; k < NT * kRowsTile; k += Roles<NT>::threads)
+                red[k] = __int_as_float(0x7FC00000);  // no sums: the results are NaN
+        }
         // each block of the cluster adds and writes its share of the tokens
         cg::cluster_group cluster = cg::this_cluster();
         cluster.sync();

@@ -313,12 +313,13 @@ __global__ void __launch_bounds__(kGvThreads, 2) q4_gemv_kernel(const __grid_con
                         const uint32_t p = t0 + 8 * k + 2 * t + (j & 1);
                         if (ok && row < L.rows && p < hi) q4_store<HALF>(A, p, row, acc[k][j]);
                     }
-            } else {
+            } else {  // (a warp that gave up has no sums: the results are NaN)
 #pragma unroll
                 for (int k = 0; k < NT; ++k)
 #pragma unroll
                     for (int j = 0; j < 4; ++j)
-                        sums[warp * Shape::vals + (k * 4 + j) * 32 + lane] = acc[k][j];
+                        sums[warp * Shape::vals + (k * 4 + j) * 32 + lane] =
+                            ok ? acc[k][j] : __int_as_float(0x7FC00000);
             }
         }
         if (P.split > 1) {
