@@ -511,7 +511,9 @@ int wc_decompress_tans_batch(const wc_batch_item *h_items, uint32_t count, int32
  *                    least wc_q4_bytes): rows d_offsets[e] .. d_offsets[e+1]-1
  *                    of x (as wc_moe_sort leaves them) take matrix e. `tokens`
  *                    bounds the rows of x and y; offsets are clamped to it, and
- *                    rows outside every range are neither read nor written.
+ *                    rows outside every range are neither read nor written. A
+ *                    row in two ranges (offsets that go back) gets either
+ *                    expert's product, element by element.
  * The expanding calls check the header on the device (WC_ERR_CORRUPT_STREAM in
  * *d_status; the output is then unspecified); of experts' streams, those whose
  * expert has rows. A product whose waits ran out (WC_ERR_TIMEOUT) leaves what it

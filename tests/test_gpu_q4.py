@@ -532,3 +532,26 @@ def test_streams_of_experts_in_a_wider_buffer(wclib, cuda):
     assert torch.equal(call(wide[:, 32:32 + size], off), y)
     assert torch.equal(call(wide[:, 32:], off), y)
     assert torch.equal(call(wide[:1, 32:32 + size + 8], off[:2]), y[:5])
+
+
+@pytest.mark.parametrize("tokens", [12, 20])
+def test_ranges_of_wild_offsets(wclib, cuda, tokens):
+    """Offsets outside the matrices and out of order, in the product of few rows
+    (12 of 3 experts) and in the other (20): the clamped ranges hold their
+    expert's product, every other row of y stays as it was."""
+    rng, m, Ws = experts_case(wclib, cuda, 3, 64, 256, 64, False, False, 5)
+    x, xd = acts(rng, tokens, 256, False, cuda)
+    status = torch.zeros(1, dtype=torch.int32, device=cuda)
+    for off in ([-5, 4, 10, 1000], [9, 3, -2**31, 7], [2**31 - 1, 0, 3, -4], [3, 5, 5, 2**31 - 1],
+                [-2**31, -1, 0, 1], [tokens, tokens + 1, 2, 9]):
+        y = torch.full((tokens + 8, 64), 7.0, device=cuda)
+        wclib.gemm_q4_experts(m, x, dev(np.array(off, np.int32), cuda), y=y[4:tokens + 4], status=status)
+        left = torch.ones(tokens + 8, dtype=torch.bool, device=cuda)
+        for e in range(3):
+            a = min(max(off[e], 0), tokens)
+            b = min(max(off[e + 1], a), tokens)
+            if b > a:
+                check(y[4 + a:4 + b], Ws[e], xd[a:b], 64, 256)
+                left[4 + a:4 + b] = False
+        assert (y[left] == 7).all()
+    assert status.item() == 0
