@@ -807,6 +807,8 @@ def _there(device: torch.device, stream):
     enqueued and tensors are allocated on."""
     if device.type != "cuda":
         raise ValueError("wcodec works on CUDA tensors; got one on %s" % device)
+    if stream is not None and stream.device != device:
+        raise ValueError("stream is on %s, not on %s" % (stream.device, device))
     with torch.cuda.device(device):
         if stream is None:
             yield

@@ -162,3 +162,12 @@ def test_experts_streams_shorter_than_their_stride(wclib):
     for whole in (big, big[:, 64:], big[:, :size], big[:1, :size + 8]):
         with pytest.raises(ValueError, match="CUDA"):
             call(whole)
+
+
+def test_a_stream_of_another_device_is_refused(wclib):
+    """(Not taken silently for the current stream of the tensors' device.)"""
+    class Stream:
+        device = torch.device("cuda", 1)
+    with pytest.raises(ValueError, match="stream is on cuda:1"):
+        with wclib._there(torch.device("cuda", 0), Stream()):
+            pass
