@@ -802,9 +802,11 @@ def _here(t: torch.Tensor, stream) -> bool:
 
 
 @contextlib.contextmanager
-def _there(device: torch.device, stream):
+def _there(device: torch.device, stream, *tensors):
     """Make ``device`` current, and ``stream`` (if given) the one that work is
-    enqueued and tensors are allocated on."""
+    enqueued and tensors are allocated on. The call's own ``tensors`` (None among
+    them) are then marked as used there, so that a caller may let go of them as
+    soon as the call returns."""
     if device.type != "cuda":
         raise ValueError("wcodec works on CUDA tensors; got one on %s" % device)
     if stream is not None and stream.device != device:
@@ -815,6 +817,9 @@ def _there(device: torch.device, stream):
         else:
             with torch.cuda.stream(stream):
                 yield
+            for t in tensors:
+                if t is not None:
+                    t.record_stream(stream)
 
 
 def _rows(t: torch.Tensor, cols: int, what: str, device=None) -> int:
@@ -908,7 +913,7 @@ def quantize_q4(w: torch.Tensor, group: int = 128, *, zeros: bool = False,
     flags = m.flags()
     size = _q4_size(rows, cols, group, flags)
     if not _here(w, stream):
-        with _there(w.device, stream):
+        with _there(w.device, stream, w, out):
             return quantize_q4(w, group, zeros=zeros, out=out)
     b = _q4_out(m, size, w)
     rc = lib().wc_q4_quantize(w.data_ptr(), ld, rows, cols, group, flags, b.data_ptr(), b.numel(),
@@ -933,7 +938,7 @@ def pack_q4(codes: torch.Tensor, scales: torch.Tensor, zeros: torch.Tensor | Non
     if zeros is not None:
         _vector(zeros, shape, torch.uint8, "zeros", codes.device)
     if not _here(codes, stream):
-        with _there(codes.device, stream):
+        with _there(codes.device, stream, codes, scales, zeros, out):
             return pack_q4(codes, scales, zeros, group=group, out=out)
     b = _q4_out(m, size, codes)
     rc = lib().wc_q4_pack(codes.data_ptr(), scales.data_ptr(),
@@ -958,7 +963,7 @@ def dequantize_q4(m: Q4Matrix, dtype: torch.dtype = torch.bfloat16, *,
     if dtype not in _DTYPES:
         raise TypeError("dequantize_q4 gives BF16, FP16 or FP32; got %s" % dtype)
     if not _here(b, stream):
-        with _there(b.device, stream):
+        with _there(b.device, stream, b, out, status):
             return dequantize_q4(m, dtype, out=out, status=status)
     if out is None:
         out = b.new_empty((rows, cols), dtype=dtype)
@@ -1001,7 +1006,7 @@ def gemm_q4(m: Q4Matrix, x: torch.Tensor, *, y: torch.Tensor | None = None,
     b = _q4_buffer(m, 1)
     tokens, ldx, ldy, flags, out_dtype = _q4_product_args(m, b, x, y, out_dtype)
     if not _here(b, stream):
-        with _there(b.device, stream):
+        with _there(b.device, stream, b, x, y, status):
             return gemm_q4(m, x, y=y, out_dtype=out_dtype, status=status)
     if y is None:
         y = x.new_empty((tokens, m.rows), dtype=out_dtype)
@@ -1027,7 +1032,7 @@ def gemm_q4_experts(m: Q4Matrix, x: torch.Tensor, offsets: torch.Tensor, *,
     if size < need:  # (the stride between streams says nothing of the last one's length)
         raise WcodecError(WC_ERR_CORRUPT_STREAM, "streams of %d bytes each; one takes %d" % (size, need))
     if not _here(b, stream):
-        with _there(b.device, stream):
+        with _there(b.device, stream, b, x, offsets, y, status):
             return gemm_q4_experts(m, x, offsets, y=y, out_dtype=out_dtype, status=status)
     if y is None:
         y = x.new_empty((tokens, m.rows), dtype=out_dtype)
@@ -1058,7 +1063,7 @@ def moe_sort(ids: torch.Tensor, experts: int, *, stream=None) -> MoePlan:
     if not 1 <= experts <= WC_MOE_MAX_EXPERTS:
         raise ValueError("1 to %d experts; got %r" % (WC_MOE_MAX_EXPERTS, experts))
     if not _here(ids, stream):
-        with _there(ids.device, stream):
+        with _there(ids.device, stream, ids):
             return moe_sort(ids, experts)
     slots = ids.numel()
     offsets = ids.new_empty(experts + 1)
@@ -1096,7 +1101,7 @@ def moe_gather(x: torch.Tensor, plan: MoePlan, *, out: torch.Tensor | None = Non
         raise ValueError("x must have %d rows" % tokens)
     ldo = cols if out is None else _moe_matrix(out, cols, "out", x)
     if not _here(x, stream):
-        with _there(x.device, stream):
+        with _there(x.device, stream, x, inv, out):
             return moe_gather(x, plan, out=out)
     if out is None:
         out = x.new_empty((tokens * top, cols))
@@ -1123,7 +1128,7 @@ def moe_combine(rows: torch.Tensor, plan: MoePlan, weights: torch.Tensor | None,
         if out.shape[0] != tokens:
             raise ValueError("out must have %d rows" % tokens)
     if not _here(rows, stream):
-        with _there(device, stream):
+        with _there(device, stream, rows, inv, weights, out):
             return moe_combine(rows, plan, weights, out=out)
     if out is None:
         out = rows.new_empty((tokens, cols))
@@ -1162,7 +1167,7 @@ def moe_combine_backward(dout: torch.Tensor, rows: torch.Tensor, plan: MoePlan,
         if drows.shape[0] != rows.shape[0]:
             raise ValueError("drows must have %d rows" % rows.shape[0])
     if not _here(rows, stream):
-        with _there(device, stream):
+        with _there(device, stream, dout, rows, inv, weights, drows):
             return moe_combine_backward(dout, rows, plan, weights, drows=drows)
     if drows is None:
         drows = rows.new_empty((rows.shape[0], cols))
