@@ -324,3 +324,55 @@ def test_sorted_rows_feed_the_products_of_streams(wclib, orc, cuda):
                 ref[t] += float(w[t, j]) * (W @ x[t].double())
                 mag[t] += float(w[t, j]) * (W.abs() @ x[t].double().abs())
     assert ((out - ref).abs() <= (d * 2.0 ** -22 + top * 2.0 ** -23 + 2.0 ** -24) * mag).all()
+
+
+def test_gradients_through_a_layer_whose_products_have_gradients(wclib, cuda):
+    """Gather and combine with their gradients inside autograd functions of the
+    caller's, around torch products of each expert's rows: the layer's gradients
+    against those of the same layer in 64 bits. All values are small integers
+    and quarters, so that every sum is exact in FP32 and the results are equal."""
+    class Gather(torch.autograd.Function):
+        @staticmethod
+        def forward(ctx, x, plan):
+            ctx.plan = plan
+            return wclib.moe_gather(x, plan, out=x.new_zeros((plan.inverse.numel(), x.shape[1])))
+
+        @staticmethod
+        def backward(ctx, drows):
+            return wclib.moe_gather_backward(drows, ctx.plan), None
+
+    class Combine(torch.autograd.Function):
+        @staticmethod
+        def forward(ctx, rows, w, plan):
+            ctx.plan = plan
+            ctx.save_for_backward(rows, w)
+            return wclib.moe_combine(rows, plan, w)
+
+        @staticmethod
+        def backward(ctx, dout):
+            rows, w = ctx.saved_tensors
+            return (*wclib.moe_combine_backward(dout, rows, ctx.plan, w, drows=torch.zeros_like(rows)), None)
+
+    rng = np.random.default_rng(31)
+    tokens, top, E, d, f = 45, 3, 5, 40, 24
+    ids = route(rng, tokens, top, E, 0.2)
+    plan = plan_of(wclib, ids, E, cuda)
+    off = plan.offsets.tolist()
+
+    def ints(*shape):
+        return torch.from_numpy(rng.integers(-3, 4, shape)).float().to(cuda)
+    x, W, w, dout = ints(tokens, d), ints(E, f, d), ints(tokens, top) / 4, ints(tokens, f)
+    a = [t.clone().requires_grad_() for t in (x, W, w)]
+    rows = Gather.apply(a[0], plan)
+    prod = torch.cat([rows[off[e]:off[e + 1]] @ a[1][e].T for e in range(E)] + [rows.new_zeros((len(rows) - off[-1], f))])
+    out = Combine.apply(prod, a[2], plan)
+    out.backward(dout)
+    b = [t.double().requires_grad_() for t in (x, W, w)]
+    kept = torch.from_numpy(ids >= 0).to(cuda)
+    every = torch.einsum("td,efd->tef", b[0], b[1])
+    picked = every[torch.arange(tokens, device=cuda)[:, None], torch.from_numpy(ids).to(cuda).clamp(min=0).long()]
+    ref = (picked * (b[2] * kept)[..., None]).sum(1)
+    ref.backward(dout.double())
+    assert torch.equal(out.double(), ref)
+    for got, want in zip(a, b):
+        assert torch.equal(got.grad.double(), want.grad)

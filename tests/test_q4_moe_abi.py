@@ -171,3 +171,32 @@ def test_a_stream_of_another_device_is_refused(wclib):
     with pytest.raises(ValueError, match="stream is on cuda:1"):
         with wclib._there(torch.device("cuda", 0), Stream()):
             pass
+
+
+def test_tensors_that_autograd_follows_are_refused(wclib):
+    """Results have no graph, so inputs and outputs that need one are refused,
+    unless gradients are off; what is left is the refusal of host tensors."""
+    m = wclib.Q4Matrix(torch.zeros(128 + 1056, dtype=torch.uint8), 4, 8, 128, False, torch.bfloat16)
+    stack = wclib.Q4Matrix(m.buffer[None], 4, 8, 128, False, torch.bfloat16)
+    plan = wclib.MoePlan(torch.zeros(3, dtype=torch.int32), None, torch.zeros((4, 2), dtype=torch.int32))
+    off = torch.tensor([0, 4], dtype=torch.int32)
+    w = torch.zeros((4, 8), dtype=torch.bfloat16)
+    g = w.clone().requires_grad_()
+    rows, grows = torch.zeros((8, 8), dtype=torch.bfloat16), torch.zeros((8, 8), dtype=torch.bfloat16, requires_grad=True)
+    gw = torch.ones((4, 2), requires_grad=True)
+    y = torch.zeros((4, 4), requires_grad=True)
+    calls = [lambda: wclib.gemm_q4(m, g), lambda: wclib.gemm_q4(m, w, y=y), lambda: wclib.gemm_q4_experts(stack, g, off),
+             lambda: wclib.dequantize_q4(m, out=g), lambda: wclib.moe_gather(g, plan),
+             lambda: wclib.moe_gather(w, plan, out=grows), lambda: wclib.moe_combine(grows, plan, None),
+             lambda: wclib.moe_combine(rows, plan, gw), lambda: wclib.moe_combine(rows, plan, None, out=g),
+             lambda: wclib.moe_gather_backward(grows, plan), lambda: wclib.moe_combine_backward(g, rows, plan, None),
+             lambda: wclib.moe_combine_backward(w, grows, plan, None),
+             lambda: wclib.moe_combine_backward(w, rows, plan, gw),
+             lambda: wclib.moe_combine_backward(w, rows, plan, None, drows=grows)]
+    for call in calls:
+        with pytest.raises(ValueError, match="autograd graph"):
+            call()
+        with pytest.raises(ValueError, match="CUDA"), torch.no_grad():
+            call()
+    with pytest.raises(ValueError, match="CUDA"):  # bytes need no graph
+        wclib.quantize_q4(g)
