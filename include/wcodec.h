@@ -519,7 +519,8 @@ int wc_decompress_tans_batch(const wc_batch_item *h_items, uint32_t count, int32
  * expert has rows. A product whose waits ran out (WC_ERR_TIMEOUT) leaves what it
  * did not finish as it was or NaN, never as partial sums. A stream shorter than
  * its size returns WC_ERR_CORRUPT_STREAM without launching. Nothing is read
- * outside the stated buffers whatever they hold.
+ * outside the stated buffers whatever they hold. Results may not share memory
+ * with inputs.
  */
 #define WC_Q4_ZEROS 1u
 #define WC_Q4_SCALES_FP16 2u
@@ -571,16 +572,17 @@ int wc_q4_gemm_experts(const void *d_streams, uint64_t stream_stride, uint32_t e
  *                    the gradient of wc_moe_gather (rows = the gradient of its
  *                    result, out = the gradient of x).
  *  wc_moe_combine_backward  the gradients of wc_moe_combine:
- *                    drows[inverse[t, j]] = weights[t, j] * dout[t] (one
- *                    rounding; rows that no slot names are left as they were)
+ *                    drows[inverse[t, j]] = weights[t, j] * dout[t] (in FP32,
+ *                    then rounded to dtype; rows that no slot names are left as
+ *                    they were)
  *                    and (may be NULL) dweights[t, j] = <dout[t], rows[...]> in
  *                    FP32 in a fixed order, 0 for a slot without a row
  * x, rows, out, dout and drows have elements of `dtype`, aligned to it, rows ld
  * elements apart; `rows` counts the rows of the sorted matrices, and an inverse
  * outside 0..rows-1 means that the slot has none. A row may be named by one slot
  * only in wc_moe_gather and wc_moe_combine_backward (as wc_moe_sort leaves it;
- * otherwise which of the slots writes it is unspecified). Every result is the
- * same on every run. No workspace.
+ * otherwise which of the slots writes it is unspecified). Results may not share
+ * memory with inputs. Every result is the same on every run. No workspace.
  */
 int wc_moe_sort(const int32_t *d_ids, uint64_t slots, uint32_t experts, int32_t *d_offsets,
                 int32_t *d_order, int32_t *d_inverse, void *stream);
