@@ -16,6 +16,8 @@ constexpr uint32_t kAllFlags = kStreamFlags | WC_Q4_X_FP16 | WC_Q4_Y_16BIT;
 // 19.6 and 17.6, 24 rows 34 and 18; 4096 x 14336, 16 rows 17.3 and 17.5; 1024 x
 // 4096, 16 rows 6.8 and 7.8, 24 rows 10.6 and 8.0. Experts (16 of 4096 x 2048),
 // whose rows come unevenly: 8 a matrix 35.5 and 33.3, 16 a matrix 43.7 and 33.9.
+// The host knows their mean alone (64 of 2048 x 1024, mean 6): all with 6 rows 29
+// and 37, half of the rows at one 112 and 41, all at one 211 and 15.
 constexpr uint64_t kFewRows = 16;
 constexpr uint64_t kFewRowsExperts = 6;
 

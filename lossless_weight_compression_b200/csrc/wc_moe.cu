@@ -5,9 +5,9 @@
 // All but the sort move each row once: a token's row is read once and written to
 // its slots' rows, or its slots' rows are read and summed, with 16-byte accesses
 // where the rows allow them. Measured (BF16; beside it the bytes at the copy's
-// rate): 16,384 tokens x 6 slots of 4 KB rows: gather 76 us (73), its gradient 79
+// rate): 16,384 tokens x 6 slots of 4 KB rows: gather 77 us (73), its gradient 79
 // us (73), sort 19 us; 8192 tokens x 2 slots of 8 KB rows: combine 40 us (31), its
-// backward 56 us (52).
+// backward 57 us (52).
 #include <cooperative_groups.h>
 
 #include <mutex>

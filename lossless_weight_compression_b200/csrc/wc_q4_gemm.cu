@@ -27,15 +27,18 @@
 // sums through distributed shared memory in a fixed order: y is the same on
 // every run. Every wait is bounded by the device timer.
 //
-// Measured (GPU time, BF16; beside it the larger of the bytes at the copy's rate
-// and the operations at the matrix product's): 64 rows of x through 14336 x 4096,
-// groups of 128, 19 us (5.1); 512 rows through 4096 x 14336, groups of 64 with zero
-// points, 69 us (35), 0.87 PFLOP/s; 2000 rows over 8 experts of 14336 x 4096, groups
-// of 128 with zero points, 258 us (137), 0.91 PFLOP/s. Bound by instruction issue
-// (0.69 a cycle and scheduler at 512 rows, of which a third is useful arithmetic,
-// the rest waits, addresses and moves around it) and, for groups of 64 and less,
-// by an accumulator's round trip of some 1000 cycles (multiply, commit, read,
-// hand back) with two of them; the tensor pipe is busy 34 % of the time. Steps on
+// Measured (GPU time of short captured runs, BF16; beside it the larger of the bytes
+// at the copy's rate and the operations at the matrix product's): 64 rows of x
+// through 14336 x 4096, groups of 128, 19.4 us (5.1); 512 rows through 4096 x 14336,
+// groups of 64 with zero points, 67 us (35), 0.89 PFLOP/s; 2000 rows over 8 experts
+// of 14336 x 4096, groups of 128 with zero points, 258 us (137), 0.91 PFLOP/s. In
+// long runs, at the power cap's clock, 77 and 310 us: 0.78 and 0.76 PFLOP/s. At 512
+// rows bound by instruction issue (0.68 a cycle and scheduler, of which a third is
+// useful arithmetic, the rest waits, addresses and moves around it) and, for groups
+// of 64 and less, by an accumulator's round trip of some 1000 cycles (multiply,
+// commit, read, hand back) with two of them; the tensor pipe is active 45 % of the
+// time. At 64 rows (issue 0.39) by the latency of a slice's chain, by fetching the
+// roles' instructions, and by 36 multiprocessors without a unit. Steps on
 // the way (512 rows): one issuing thread, 8 + 8 warps 135 us; two issuing warps 104;
 // no time limits inside polls, uniform issuing 91; one barrier a group 77; sums by
 // 16 warps, pairs scaled where they were read 73; barrier addresses kept in

@@ -15,11 +15,13 @@
 // take one 16-row record each, so that the only sum across warps is the
 // cluster's, over its blocks in a fixed order.
 //
-// Measured (GPU time, groups of 128, BF16; beside it the time of the bytes at the
-// copy's rate): 1 row of x through 4096 x 4096 6.3 us (1.3), through 4096 x 14336
-// 13.5 us (4.7); 8 rows through 14336 x 4096 15.9 us (4.7), 16 rows 20 us; 48 rows
-// over 43 of 64 experts of 2048 x 1024 17 us (8.3). Bound by the warps' chains of
-// unpacking and multiplying (issue 53 %), and the smallest by a launch's latency.
+// Measured (GPU time, groups of 128, BF16, weights from HBM; beside it the time of
+// the bytes at the copy's rate): 1 row of x through 4096 x 4096 7.0 us (1.3), 6.3
+// from L2; through 4096 x 14336 12.8 us (4.7); 8 rows through 14336 x 4096 15.4 us
+// (4.7), 16 rows 19.4 us; 48 rows over 64 experts of 2048 x 1024 16.9 us (8.3).
+// From L2 instead they take 2 to 8 % less: bound by the warps' chains of unpacking
+// and multiplying (issue 0.31 to 0.50 a cycle) and by each block's start, first
+// loads and tail, which come once for every 35 to 135 KB of the stream.
 // Loads straight into registers, with a row's slices spread over a block's warps,
 // were 10 % faster for one row of x through 4096 x 4096, 10 to 60 % slower for
 // experts and for 16 rows. Two sums a group instead of one, for shorter chains of
