@@ -825,13 +825,13 @@ def _there(device: torch.device, stream, *tensors):
                     t.record_stream(stream)
 
 
-def _no_graph(what: str, *tensors):
-    """Refuse tensors (None among them) that autograd would follow: results here have
-    no graph, and the gradient would be lost without a word."""
-    for t in tensors:
-        if t is not None and t.requires_grad and torch.is_grad_enabled():
-            raise ValueError("%s records no autograd graph: call it under torch.no_grad(), or on detached "
-                             "tensors" % what)
+def _no_graph(what: str):
+    """For a call some of whose tensors require grad: refused where autograd would
+    follow them. Results here have no graph, and the gradient would be lost without
+    a word."""
+    if torch.is_grad_enabled():
+        raise ValueError("%s records no autograd graph: call it under torch.no_grad(), or on detached tensors"
+                         % what)
 
 
 def _rows(t: torch.Tensor, cols: int, what: str, device=None) -> int:
@@ -974,7 +974,8 @@ def dequantize_q4(m: Q4Matrix, dtype: torch.dtype = torch.bfloat16, *,
             raise ValueError("out must have %d rows" % rows)
     if dtype not in _DTYPES:
         raise TypeError("dequantize_q4 gives BF16, FP16 or FP32; got %s" % dtype)
-    _no_graph("dequantize_q4", out)
+    if out is not None and out.requires_grad:
+        _no_graph("dequantize_q4")
     if not _here(b, stream):
         with _there(b.device, stream, b, out, status):
             return dequantize_q4(m, dtype, out=out, status=status)
@@ -1018,7 +1019,8 @@ def gemm_q4(m: Q4Matrix, x: torch.Tensor, *, y: torch.Tensor | None = None,
     FP16, y (tokens, rows) in FP32 or x's type."""
     b = _q4_buffer(m, 1)
     tokens, ldx, ldy, flags, out_dtype = _q4_product_args(m, b, x, y, out_dtype)
-    _no_graph("gemm_q4", x, y)
+    if x.requires_grad or (y is not None and y.requires_grad):
+        _no_graph("gemm_q4")
     if not _here(b, stream):
         with _there(b.device, stream, b, x, y, status):
             return gemm_q4(m, x, y=y, out_dtype=out_dtype, status=status)
@@ -1042,10 +1044,11 @@ def gemm_q4_experts(m: Q4Matrix, x: torch.Tensor, offsets: torch.Tensor, *,
     experts, size = b.shape
     _vector(offsets, (experts + 1,), torch.int32, "offsets", b.device)
     tokens, ldx, ldy, flags, out_dtype = _q4_product_args(m, b, x, y, out_dtype)
-    need = _q4_size(m.rows, m.cols, m.group, m.flags())
+    need = _q4_size(m.rows, m.cols, m.group, flags & (WC_Q4_ZEROS | WC_Q4_SCALES_FP16))
     if size < need:  # (the stride between streams says nothing of the last one's length)
         raise WcodecError(WC_ERR_CORRUPT_STREAM, "streams of %d bytes each; one takes %d" % (size, need))
-    _no_graph("gemm_q4_experts", x, y)
+    if x.requires_grad or (y is not None and y.requires_grad):
+        _no_graph("gemm_q4_experts")
     if not _here(b, stream):
         with _there(b.device, stream, b, x, offsets, y, status):
             return gemm_q4_experts(m, x, offsets, y=y, out_dtype=out_dtype, status=status)
@@ -1115,7 +1118,8 @@ def moe_gather(x: torch.Tensor, plan: MoePlan, *, out: torch.Tensor | None = Non
     if x.shape[0] != tokens:
         raise ValueError("x must have %d rows" % tokens)
     ldo = cols if out is None else _moe_matrix(out, cols, "out", x)
-    _no_graph("moe_gather", x, out)
+    if x.requires_grad or (out is not None and out.requires_grad):
+        _no_graph("moe_gather")
     if not _here(x, stream):
         with _there(x.device, stream, x, inv, out):
             return moe_gather(x, plan, out=out)
@@ -1143,7 +1147,8 @@ def moe_combine(rows: torch.Tensor, plan: MoePlan, weights: torch.Tensor | None,
         ldo = _moe_matrix(out, cols, "out", rows)
         if out.shape[0] != tokens:
             raise ValueError("out must have %d rows" % tokens)
-    _no_graph("moe_combine", rows, weights, out)
+    if rows.requires_grad or (weights is not None and weights.requires_grad) or (out is not None and out.requires_grad):
+        _no_graph("moe_combine")
     if not _here(rows, stream):
         with _there(device, stream, rows, inv, weights, out):
             return moe_combine(rows, plan, weights, out=out)
@@ -1183,7 +1188,9 @@ def moe_combine_backward(dout: torch.Tensor, rows: torch.Tensor, plan: MoePlan,
         lddr = _moe_matrix(drows, cols, "drows", rows)
         if drows.shape[0] != rows.shape[0]:
             raise ValueError("drows must have %d rows" % rows.shape[0])
-    _no_graph("moe_combine_backward", dout, rows, weights, drows)
+    if dout.requires_grad or rows.requires_grad or (weights is not None and weights.requires_grad) or \
+            (drows is not None and drows.requires_grad):
+        _no_graph("moe_combine_backward")
     if not _here(rows, stream):
         with _there(device, stream, dout, rows, inv, weights, drows):
             return moe_combine_backward(dout, rows, plan, weights, drows=drows)
