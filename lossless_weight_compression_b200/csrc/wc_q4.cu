@@ -9,10 +9,10 @@
 // is read once and each stream byte written once. Measured (14336 x 4096 BF16,
 // groups of 128): quantizing 42 us, 3.5 TB/s of the 6.5 a copy moves, bound by
 // instruction issue (0.79 a cycle, about 13 instructions a weight); expanding 27 us,
-// 5.5 TB/s, from L2 or HBM, issue 0.79 as well. Both together 65 us (119 us with a division, a
-// rintf and a conversion to int for each weight); 1000 x 4100 FP16, groups of 32
-// with zero points, 10 us (35 us while groups of zeros and a ragged last slice
-// took the slow paths).
+// 5.5 TB/s, from L2 or HBM, issue 0.79 as well. Both together 65 us (119 us with a
+// division, a rintf and a conversion to int for each weight); 1000 x 4100 FP16,
+// groups of 32 with zero points, 10 us (35 us while groups of zeros and a ragged
+// last slice took the slow paths).
 #include "wc_q4_core.cuh"
 
 namespace wc {
